@@ -64,7 +64,11 @@ typedef enum {
                                   array of wkv7_backward_noalloc holds       */
 } wkv7_status;
 
-typedef enum { WKV7_F32 = 0, WKV7_BF16 = 1 } wkv7_dtype;
+typedef enum {
+    WKV7_F32 = 0,
+    WKV7_BF16 = 1,
+    WKV7_E4M3 = 2   /* 8-bit codes with block scales: only where wkv7_ssm.h says so */
+} wkv7_dtype;
 
 typedef enum {
     WKV7_ALGO_AUTO = 0,   /* library picks: CHUNK for bf16 inputs when T >= 64, else SEQ */

@@ -23,7 +23,7 @@ NVCC_FLAGS = [
 
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh")) +
-                  [os.path.join(INCLUDE, "wkv7.h")])
+                  glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def needs_build() -> bool:

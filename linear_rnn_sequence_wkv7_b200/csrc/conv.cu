@@ -1,0 +1,550 @@
+// Short causal convolution (width 2 to 4), its single-token step and its
+// backward.
+//
+//     p_t = bias + sum_j w_j x_{t-W+1+j},  y_t = p_t sigmoid(p_t)  (or p_t)
+//     dp_t = dy_t act'(p_t),  dx_t = sum_j w_j dp_{t+W-1-j},  dw_j = sum_t dp_t x_{t-W+1+j}
+//
+// All three are bound by memory (2 + 2 bytes a bf16 element forward).  A warp
+// holds a block of 128 channels, four a lane, and walks a run of tokens with
+// the last W - 1 inputs in registers, so an input is read once and W - 1 halo
+// tokens more a run; the 8-bit activation's scale belongs to exactly that block.
+#include <type_traits>
+
+#include "mixer.cuh"
+
+namespace wkv7 {
+namespace mixer {
+
+void sum_parts(long long parts, long long cols, const float *partial, float *out, cudaStream_t st);
+
+namespace {
+
+constexpr int kConvWarps = 4;       // forward: warps a block, each a run of its own
+constexpr int kConvRun = 32;        // tokens a run
+constexpr int kConvAhead = 4;       // tokens whose loads are issued together
+
+// Four channels of one token: raw words, and the scale when they are codes
+template <typename T, bool VEC> struct Token {
+    Vec<T, VEC ? 4 : 1> v[VEC ? 1 : 4];
+    float scale;
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (auto &e : v) e.zero();
+        scale = 0.f;
+    }
+    __device__ __forceinline__ void load(const T *row, const float *scales, int blk, int lane, int D) {
+#pragma unroll
+        for (int i = 0; i < (VEC ? 1 : 4); ++i) {
+            v[i].zero();
+            const int c = lane_channel<VEC>(blk, lane, i);
+            if (c < D) v[i].load(row + c);
+        }
+        if constexpr (sizeof(T) == 1) scale = __ldg(scales);
+    }
+    __device__ __forceinline__ void get(float (&f)[4]) const {
+        if constexpr (VEC) v[0].get(f);
+        else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float g[1];
+                v[i].get(g);
+                f[i] = g[0];
+            }
+        }
+        if constexpr (sizeof(T) == 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] *= scale;
+        }
+    }
+};
+
+template <bool VEC, typename T>
+__device__ __forceinline__ void load4c(const T *row, int blk, int lane, int D, float (&f)[4]) {
+    row_load<VEC>(row, blk, lane, D, f);
+}
+
+template <int W, bool VEC>
+__device__ __forceinline__ void load_params(const float *weight, const float *bias, int blk, int lane, int D,
+                                            float (&w)[W][4], float (&b)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = lane_channel<VEC>(blk, lane, i);
+        b[i] = (bias && c < D) ? __ldg(bias + c) : 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) w[j][i] = c < D ? __ldg(weight + (size_t)c * W + j) : 0.f;
+    }
+}
+
+struct ConvFwd {
+    int B, T, D;
+    const void *x;
+    long long x_bs, x_ts;
+    const float *x_scales;
+    const float *weight, *bias;
+    const void *state;
+    const int *lens;
+    int silu;
+    void *y, *state_out;
+    uint8_t *codes;
+    float *scales;
+    int runs;
+};
+
+// ST: the state's type (x's, or y's when x is codes).  SAVE: x's codes go out too.
+template <typename T, typename ST, typename YT, int W, bool VEC, bool SAVE>
+__global__ void __launch_bounds__(32 * kConvWarps)
+conv_fwd_kernel(const ConvFwd P) {
+    constexpr bool PRECISE = sizeof(YT) == 4;
+    const int lane = threadIdx.x & 31, D = P.D, nblk = (D + kBlk - 1) / kBlk;
+    const long long unit = (long long)blockIdx.x * kConvWarps + (threadIdx.x >> 5);
+    const int blk = (int)(unit % nblk);
+    const long long rest = unit / nblk;
+    const int run = (int)(rest % P.runs);
+    const long long b = rest / P.runs;
+    if (b >= P.B) return;
+    int len = P.T;
+    if (P.lens) len = min(max(__ldg(P.lens + b), 0), P.T);
+    const int t0 = run * kConvRun, t1 = min(t0 + kConvRun, len);
+    const T *x = static_cast<const T *>(P.x) + b * P.x_bs;
+    const ST *state = static_cast<const ST *>(P.state);
+    const float *xs = sizeof(T) == 1 ? P.x_scales + b * P.T * nblk + blk : nullptr;
+    auto past = [&](int t, float (&f)[4]) {         // x at t >= -(W - 1), t < len
+        if (t >= 0) {
+            Token<T, VEC> k;
+            k.load(x + t * P.x_ts, xs + (long long)t * nblk, blk, lane, D);
+            k.get(f);
+        } else if (state) {
+            load4c<VEC>(state + (b * (W - 1) + (t + W - 1)) * D, blk, lane, D, f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = 0.f;
+        }
+    };
+    if constexpr (sizeof(T) > 1) {
+        if (P.state_out && run == 0) {              // the last W - 1 inputs of the sequence, as they are
+            T *so = static_cast<T *>(P.state_out);
+#pragma unroll
+            for (int j = 0; j < W - 1; ++j) {
+                float f[4];
+                past(len - (W - 1) + j, f);
+                row_store<VEC>(so + (b * (W - 1) + j) * D, blk, lane, D, f);
+            }
+        }
+    }
+    if (t0 >= t1) return;
+    float w[W][4], bias[4];
+    load_params<W, VEC>(P.weight, P.bias, blk, lane, D, w, bias);
+    float h[W - 1][4];                              // the last W - 1 inputs, oldest first
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) past(t0 - (W - 1) + j, h[j]);
+    YT *y = static_cast<YT *>(P.y) + b * P.T * (long long)D;
+    Token<T, VEC> next[kConvAhead];
+#pragma unroll
+    for (int k = 0; k < kConvAhead; ++k)
+        if (t0 + k < t1) next[k].load(x + (t0 + k) * P.x_ts, xs + (long long)(t0 + k) * nblk, blk, lane, D);
+    for (int t = t0; t < t1; t += kConvAhead) {
+        Token<T, VEC> now[kConvAhead];
+#pragma unroll
+        for (int k = 0; k < kConvAhead; ++k) now[k] = next[k];
+#pragma unroll
+        for (int k = 0; k < kConvAhead; ++k)
+            if (t + kConvAhead + k < t1)
+                next[k].load(x + (t + kConvAhead + k) * P.x_ts, xs + (long long)(t + kConvAhead + k) * nblk, blk, lane, D);
+#pragma unroll
+        for (int k = 0; k < kConvAhead; ++k) {
+            if (t + k >= t1) break;
+            float v[4], o[4];
+            now[k].get(v);
+            if constexpr (SAVE) {
+                uint32_t q;
+                const float scale = act8_encode(v, q);
+                const long long r = b * P.T + t + k;
+                row_store_codes<VEC>(P.codes + r * D, blk, lane, D, q);
+                if (lane == 0) P.scales[r * nblk + blk] = scale;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float p = fmaf(w[W - 1][i], v[i], bias[i]);
+#pragma unroll
+                for (int j = W - 2; j >= 0; --j) p = fmaf(w[j][i], h[j][i], p);
+                o[i] = P.silu ? p * sigmoid<PRECISE>(p) : p;
+#pragma unroll
+                for (int j = 0; j < W - 2; ++j) h[j][i] = h[j + 1][i];
+                h[W - 2][i] = v[i];
+            }
+            row_store<VEC>(y + (long long)(t + k) * D, blk, lane, D, o);
+        }
+    }
+}
+
+// One token: a thread per channel, its W - 1 state values moved on in place.
+template <typename T, typename YT, int W>
+__global__ void __launch_bounds__(256)
+conv_step_kernel(long long total, int D, const T *__restrict__ x, long long x_bs, const float *__restrict__ weight,
+                 const float *__restrict__ bias, T *state, int silu, YT *__restrict__ y) {
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (id >= total) return;
+    const long long b = id / D;
+    const int c = (int)(id % D);
+    T *s = state + b * (W - 1) * D + c;
+    T h[W - 1];
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) h[j] = s[(size_t)j * D];
+    const T in = x[b * x_bs + c];
+    float p = fmaf(__ldg(weight + (size_t)c * W + W - 1), to_f32(in), bias ? __ldg(bias + c) : 0.f);
+#pragma unroll
+    for (int j = W - 2; j >= 0; --j) p = fmaf(__ldg(weight + (size_t)c * W + j), to_f32(h[j]), p);
+#pragma unroll
+    for (int j = 0; j < W - 2; ++j) s[(size_t)j * D] = h[j + 1];
+    s[(size_t)(W - 2) * D] = in;
+    y[id] = from_f32<YT>(silu ? p * sigmoid<sizeof(YT) == 4>(p) : p);
+}
+
+constexpr int kConvBwdWarps = 8;    // backward: runs a block, joined in shared memory
+constexpr int kConvBwdRun = 64;     // tokens a run
+
+struct ConvBwd {
+    int B, T, D;
+    const void *x;
+    long long x_bs, x_ts;
+    const float *x_scales;
+    const float *weight, *bias;
+    const void *state, *dy;
+    const float *dstate_out;
+    int silu;
+    void *dx;
+    float *dstate;
+    float *partial;                 // [B * groups][W + 1][D]
+    int groups;                     // blocks of runs a sequence
+};
+
+// A warp's run of tokens [t0, t1): at token t it has p_t and dp_t, hence
+// dx_{t-W+1} = sum_j w_j dp_{t-j}; W - 1 tokens behind the run give the rest.
+template <typename T, typename ST, typename DT, typename GT, int W, bool VEC>
+__global__ void __launch_bounds__(32 * kConvBwdWarps)
+conv_bwd_kernel(const ConvBwd P) {
+    constexpr bool PRECISE = sizeof(GT) == 4;
+    __shared__ float part[kConvBwdWarps][W + 1][kBlk];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = P.D, nblk = (D + kBlk - 1) / kBlk;
+    const int blk = (int)(blockIdx.x % nblk);
+    const long long rest = blockIdx.x / nblk;
+    const int group = (int)(rest % P.groups);
+    const long long b = rest / P.groups;
+    const int t0 = min((group * kConvBwdWarps + warp) * kConvBwdRun, P.T), t1 = min(t0 + kConvBwdRun, P.T);
+    const bool first = t0 == 0 && warp == 0 && group == 0;
+    const T *x = static_cast<const T *>(P.x) + b * P.x_bs;
+    const ST *state = static_cast<const ST *>(P.state);
+    const DT *dy = static_cast<const DT *>(P.dy) + b * P.T * (long long)D;
+    GT *dx = static_cast<GT *>(P.dx) + b * P.T * (long long)D;
+    const float *xs = sizeof(T) == 1 ? P.x_scales + b * P.T * nblk + blk : nullptr;
+    float w[W][4], bias[4], dw[W][4], db[4];
+    load_params<W, VEC>(P.weight, P.bias, blk, lane, D, w, bias);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        db[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+    }
+    if (t0 < t1) {
+        float h[W][4], dp[W][4];                    // x and dp at t - W + 1 .. t
+#pragma unroll
+        for (int j = 0; j < W; ++j) {
+            const int t = t0 - W + j;               // shifted once before the first token
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dp[j][i] = h[j][i] = 0.f;
+            if (j > 0 && t >= 0) {
+                Token<T, VEC> k;
+                k.load(x + t * P.x_ts, xs + (long long)t * nblk, blk, lane, D);
+                k.get(h[j]);
+            } else if (j > 0 && state) {
+                load4c<VEC>(state + (b * (W - 1) + (t + W - 1)) * D, blk, lane, D, h[j]);
+            }
+        }
+        const int end = t1 + W - 1;
+        for (int tt = t0; tt < end; tt += kConvAhead) {
+            Token<T, VEC> xr[kConvAhead];
+            Token<DT, VEC> gr[kConvAhead];
+#pragma unroll
+            for (int k = 0; k < kConvAhead; ++k) {
+                xr[k].zero();
+                gr[k].zero();
+                const int t = tt + k;
+                if (t < end && t < P.T) {
+                    xr[k].load(x + t * P.x_ts, xs + (long long)t * nblk, blk, lane, D);
+                    gr[k].load(dy + (long long)t * D, nullptr, blk, lane, D);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kConvAhead; ++k) {
+                const int t = tt + k;
+                if (t >= end) break;
+                float v[4], g[4], o[4];
+                xr[k].get(v);
+                gr[k].get(g);
+                const bool live = t < t1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int j = 0; j < W - 1; ++j) h[j][i] = h[j + 1][i], dp[j][i] = dp[j + 1][i];
+                    h[W - 1][i] = v[i];
+                    float e = t < P.T ? g[i] : 0.f;
+                    if (P.silu) {
+                        float p = bias[i];
+#pragma unroll
+                        for (int j = W - 1; j >= 0; --j) p = fmaf(w[j][i], h[j][i], p);
+                        const float sg = sigmoid<PRECISE>(p);
+                        e = t < P.T ? e * sg * fmaf(p, 1.f - sg, 1.f) : 0.f;
+                    }
+                    dp[W - 1][i] = e;
+                    if (live) {
+                        db[i] += e;
+#pragma unroll
+                        for (int j = 0; j < W; ++j) dw[j][i] = fmaf(e, h[j][i], dw[j][i]);
+                    }
+                    float d = 0.f;
+#pragma unroll
+                    for (int j = 0; j < W; ++j) d = fmaf(w[j][i], dp[W - 1 - j][i], d);
+                    o[i] = d;
+                }
+                const int at = t - (W - 1);         // the token whose gradient is complete
+                const int row = at - (P.T - (W - 1));
+                if (P.dstate_out && row >= 0) {     // it is in state_out as well
+                    float f[4];
+                    load4c<VEC>(P.dstate_out + (b * (W - 1) + row) * D, blk, lane, D, f);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[i] += f[i];
+                }
+                if (at >= t0) row_store<VEC>(dx + (long long)at * D, blk, lane, D, o);
+                else if (first && P.dstate) row_store<VEC>(P.dstate + (b * (W - 1) + at + W - 1) * D, blk, lane, D, o);
+            }
+        }
+    }
+    // the block's runs, in order
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int c = lane_channel<VEC>(0, lane, i);
+#pragma unroll
+        for (int j = 0; j < W; ++j) part[warp][j][c] = dw[j][i];
+        part[warp][W][c] = db[i];
+    }
+    __syncthreads();
+    float *out = P.partial + (b * P.groups + group) * (W + 1) * (long long)D;
+    for (int e = threadIdx.x; e < (W + 1) * kBlk; e += blockDim.x) {
+        const int j = e / kBlk, c = e % kBlk;
+        if (blk * kBlk + c >= D) continue;
+        float a = part[0][j][c];
+#pragma unroll
+        for (int k = 1; k < kConvBwdWarps; ++k) a += part[k][j][c];
+        out[(long long)j * D + blk * kBlk + c] = a;
+    }
+}
+
+// [W + 1][D] sums -> dweight [D][W] and dbias [D]
+__global__ void conv_params_kernel(int D, int W, const float *__restrict__ sums, float *__restrict__ dweight,
+                                   float *__restrict__ dbias) {
+    const int e = blockIdx.x * blockDim.x + threadIdx.x;
+    if (e >= D * (W + 1)) return;
+    const int j = e / D, c = e % D;
+    if (j < W) dweight[(size_t)c * W + j] = sums[e];
+    else if (dbias) dbias[c] = sums[e];
+}
+
+wkv7_status conv_dims(int B, int T, int D, int W) {
+    if (B < 0 || T < 0 || D < 0 || W <= 0) return WKV7_ERR_INVALID_ARG;
+    if (W < 2 || W > 4 || D > WKV7_SSM_MAX_D || T > kMaxTokens) return WKV7_ERR_UNSUPPORTED;
+    const long long runs = ((long long)T + kConvRun - 1) / kConvRun + 1;
+    // blocks of a launch, and of the step's
+    if ((double)B * runs * blocks_of(D) > (double)kMaxGrid) return WKV7_ERR_UNSUPPORTED;
+    return WKV7_OK;
+}
+
+int conv_groups(int T) {
+    const int per = kConvBwdWarps * kConvBwdRun;
+    return (int)(((long long)T + per - 1) / per);
+}
+
+// width as a template argument, then the rest of the launch
+template <typename F> void by_width(int W, F &&f) {
+    if (W == 2) f(std::integral_constant<int, 2>{});
+    else if (W == 3) f(std::integral_constant<int, 3>{});
+    else f(std::integral_constant<int, 4>{});
+}
+
+template <typename T, typename ST, typename YT, bool SAVE>
+void launch_conv_fwd(const ConvFwd &P, int W, bool vec, cudaStream_t st) {
+    const long long units = (long long)P.B * P.runs * blocks_of(P.D);
+    const unsigned grid = (unsigned)((units + kConvWarps - 1) / kConvWarps);
+    by_width(W, [&](auto w) {
+        if (vec) conv_fwd_kernel<T, ST, YT, decltype(w)::value, true, SAVE><<<grid, 32 * kConvWarps, 0, st>>>(P);
+        else conv_fwd_kernel<T, ST, YT, decltype(w)::value, false, SAVE><<<grid, 32 * kConvWarps, 0, st>>>(P);
+    });
+}
+
+template <typename T, typename ST, typename DT, typename GT>
+void launch_conv_bwd(const ConvBwd &P, int W, bool vec, cudaStream_t st) {
+    const unsigned grid = (unsigned)((long long)P.B * P.groups * blocks_of(P.D));
+    by_width(W, [&](auto w) {
+        if (vec) conv_bwd_kernel<T, ST, DT, GT, decltype(w)::value, true><<<grid, 32 * kConvBwdWarps, 0, st>>>(P);
+        else conv_bwd_kernel<T, ST, DT, GT, decltype(w)::value, false><<<grid, 32 * kConvBwdWarps, 0, st>>>(P);
+    });
+}
+
+}  // namespace
+}  // namespace mixer
+}  // namespace wkv7
+
+extern "C" {
+
+wkv7_status wkv7_conv_forward(int B, int T, int D, int W, wkv7_dtype x_dt, wkv7_dtype y_dt, const void *x,
+                              long long x_bs, long long x_ts, const float *x_scales, const float *weight,
+                              const float *bias, const void *state, const int *lens, int silu, void *y,
+                              void *state_out, void *codes, float *scales, cudaStream_t stream) {
+    using namespace wkv7::mixer;
+    const wkv7_status st = conv_dims(B, T, D, W);
+    if (st != WKV7_OK) return st;
+    const bool q8 = x_dt == WKV7_E4M3;
+    if (!(real_dtype(x_dt) || q8) || !real_dtype(y_dt) || x_bs < 0 || x_ts < 0) return WKV7_ERR_INVALID_ARG;
+    if ((codes != nullptr) != (scales != nullptr)) return WKV7_ERR_INVALID_ARG;
+    if ((q8 || lens) && codes) return WKV7_ERR_INVALID_ARG;
+    if (q8 && state_out) return WKV7_ERR_INVALID_ARG;
+    if (state_out && state_out == state) return WKV7_ERR_INVALID_ARG;
+    if (B == 0 || D == 0) return WKV7_OK;
+    const wkv7_dtype s_dt = q8 ? y_dt : x_dt;
+    if (T > 0 && (!elem_ok(x, x_dt) || !elem_ok(y, y_dt))) return WKV7_ERR_INVALID_ARG;
+    if (q8 != (x_scales != nullptr) || !f32_opt(x_scales)) return WKV7_ERR_INVALID_ARG;
+    if (!f32_ok(weight) || !f32_opt(bias) || !f32_opt(scales) || !aligned_to(lens, 4) ||
+        !aligned_to(state, dtype_size(s_dt)) || !aligned_to(state_out, dtype_size(s_dt)))
+        return WKV7_ERR_INVALID_ARG;
+    if (T == 0 && !state_out) return WKV7_OK;
+    if (q8) x_bs = (long long)T * D, x_ts = D;
+    int runs = (int)(((long long)T + kConvRun - 1) / kConvRun);
+    if (runs == 0) runs = 1;                        // T = 0: the state alone
+    const ConvFwd P{B, T, D, x, x_bs, x_ts, x_scales, weight, bias, state, lens, silu, y, state_out,
+                    (uint8_t *)codes, scales, runs};
+    const bool vec = D % 4 == 0 && x_bs % 4 == 0 && x_ts % 4 == 0 && aligned_to(x, 4 * dtype_size(x_dt)) &&
+                     aligned_to(y, 4 * dtype_size(y_dt)) && aligned_to(state, 4 * dtype_size(s_dt)) &&
+                     aligned_to(state_out, 4 * dtype_size(s_dt)) && aligned_to(codes, 4);
+    const bool yf = y_dt == WKV7_F32;
+    if (q8) {
+        if (yf) launch_conv_fwd<e4m3, float, float, false>(P, W, vec, stream);
+        else launch_conv_fwd<e4m3, bf16, bf16, false>(P, W, vec, stream);
+    } else if (x_dt == WKV7_F32) {
+        if (codes) {
+            if (yf) launch_conv_fwd<float, float, float, true>(P, W, vec, stream);
+            else launch_conv_fwd<float, float, bf16, true>(P, W, vec, stream);
+        } else {
+            if (yf) launch_conv_fwd<float, float, float, false>(P, W, vec, stream);
+            else launch_conv_fwd<float, float, bf16, false>(P, W, vec, stream);
+        }
+    } else {
+        if (codes) {
+            if (yf) launch_conv_fwd<bf16, bf16, float, true>(P, W, vec, stream);
+            else launch_conv_fwd<bf16, bf16, bf16, true>(P, W, vec, stream);
+        } else {
+            if (yf) launch_conv_fwd<bf16, bf16, float, false>(P, W, vec, stream);
+            else launch_conv_fwd<bf16, bf16, bf16, false>(P, W, vec, stream);
+        }
+    }
+    return launch_status();
+}
+
+wkv7_status wkv7_conv_step(int B, int D, int W, wkv7_dtype x_dt, wkv7_dtype y_dt, const void *x, long long x_bs,
+                           const float *weight, const float *bias, void *state, int silu, void *y,
+                           cudaStream_t stream) {
+    using namespace wkv7::mixer;
+    const wkv7_status st = conv_dims(B, 1, D, W);
+    if (st != WKV7_OK) return st;
+    if (!real_dtype(x_dt) || !real_dtype(y_dt) || x_bs < 0) return WKV7_ERR_INVALID_ARG;
+    if (B == 0 || D == 0) return WKV7_OK;
+    if (!elem_ok(x, x_dt) || !elem_ok(y, y_dt) || !elem_ok(state, x_dt) || !f32_ok(weight) || !f32_opt(bias))
+        return WKV7_ERR_INVALID_ARG;
+    const long long total = (long long)B * D;
+    const unsigned grid = (unsigned)((total + 255) / 256);
+    by_width(W, [&](auto w) {
+        constexpr int WW = decltype(w)::value;
+#define WKV7_STEP(I, O)                                                                                        \
+    conv_step_kernel<I, O, WW><<<grid, 256, 0, stream>>>(total, D, (const I *)x, x_bs, weight, bias, (I *)state, \
+                                                         silu, (O *)y)
+        if (x_dt == WKV7_F32 && y_dt == WKV7_F32) WKV7_STEP(float, float);
+        else if (x_dt == WKV7_F32) WKV7_STEP(float, bf16);
+        else if (y_dt == WKV7_F32) WKV7_STEP(bf16, float);
+        else WKV7_STEP(bf16, bf16);
+#undef WKV7_STEP
+    });
+    return launch_status();
+}
+
+size_t wkv7_conv_backward_workspace_size(int B, int T, int D, int W) {
+    using namespace wkv7::mixer;
+    if (B <= 0 || T <= 0 || D <= 0 || conv_dims(B, T, D, W) != WKV7_OK) return 0;
+    const size_t cols = (size_t)D * (W + 1);
+    return round256((size_t)B * conv_groups(T) * cols * sizeof(float)) + round256(cols * sizeof(float));
+}
+
+wkv7_status wkv7_conv_backward(int B, int T, int D, int W, wkv7_dtype x_dt, wkv7_dtype dy_dt, wkv7_dtype g_dt,
+                               const void *x, long long x_bs, long long x_ts, const float *x_scales,
+                               const float *weight, const float *bias, const void *state, const void *dy,
+                               const float *dstate_out, int silu, void *dx, float *dweight, float *dbias,
+                               float *dstate, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    using namespace wkv7::mixer;
+    const wkv7_status st = conv_dims(B, T, D, W);
+    if (st != WKV7_OK) return st;
+    const bool q8 = x_dt == WKV7_E4M3;
+    if (!(real_dtype(x_dt) || q8) || !real_dtype(dy_dt) || !real_dtype(g_dt) || x_bs < 0 || x_ts < 0)
+        return WKV7_ERR_INVALID_ARG;
+    if (D == 0) return WKV7_OK;
+    if (!f32_ok(dweight) || !f32_opt(dbias) || !f32_opt(dstate) || !f32_opt(dstate_out)) return WKV7_ERR_INVALID_ARG;
+    if (B == 0 || T == 0) {
+        if (cudaMemsetAsync(dweight, 0, (size_t)D * W * 4, stream) != cudaSuccess) return WKV7_ERR_CUDA;
+        if (dbias && cudaMemsetAsync(dbias, 0, (size_t)D * 4, stream) != cudaSuccess) return WKV7_ERR_CUDA;
+        const size_t n = (size_t)B * (W - 1) * D * 4;       // without a token state_out is state
+        if (dstate && n && dstate != dstate_out) {
+            const cudaError_t e = dstate_out ? cudaMemcpyAsync(dstate, dstate_out, n, cudaMemcpyDeviceToDevice, stream)
+                                             : cudaMemsetAsync(dstate, 0, n, stream);
+            if (e != cudaSuccess) return WKV7_ERR_CUDA;
+        }
+        return WKV7_OK;
+    }
+    const wkv7_dtype s_dt = q8 ? g_dt : x_dt;
+    if (!elem_ok(x, x_dt) || !elem_ok(dy, dy_dt) || !elem_ok(dx, g_dt) || !f32_ok(weight) || !f32_opt(bias) ||
+        q8 != (x_scales != nullptr) || !f32_opt(x_scales) || !aligned_to(state, dtype_size(s_dt)))
+        return WKV7_ERR_INVALID_ARG;
+    if (dstate && dstate == dstate_out) return WKV7_ERR_INVALID_ARG;
+    if (workspace == nullptr || !aligned_to(workspace, 16) ||
+        workspace_bytes < wkv7_conv_backward_workspace_size(B, T, D, W))
+        return WKV7_ERR_INVALID_ARG;
+    if (q8) x_bs = (long long)T * D, x_ts = D;
+    const int groups = conv_groups(T);
+    const size_t cols = (size_t)D * (W + 1);
+    float *partial = (float *)workspace;
+    float *sums = (float *)((char *)workspace + round256((size_t)B * groups * cols * sizeof(float)));
+    const ConvBwd P{B, T, D, x, x_bs, x_ts, x_scales, weight, bias, state, dy, dstate_out, silu, dx, dstate, partial,
+                    groups};
+    const bool vec = D % 4 == 0 && x_bs % 4 == 0 && x_ts % 4 == 0 && aligned_to(x, 4 * dtype_size(x_dt)) &&
+                     aligned_to(dy, 4 * dtype_size(dy_dt)) && aligned_to(dx, 4 * dtype_size(g_dt)) &&
+                     aligned_to(state, 4 * dtype_size(s_dt)) && aligned_to(dstate, 16) && aligned_to(dstate_out, 16);
+    const bool df = dy_dt == WKV7_F32, gf = g_dt == WKV7_F32;
+#define WKV7_BWD(T, ST, DT, GT) launch_conv_bwd<T, ST, DT, GT>(P, W, vec, stream)
+    if (q8) {
+        if (df && gf) WKV7_BWD(e4m3, float, float, float);
+        else if (df) WKV7_BWD(e4m3, bf16, float, bf16);
+        else if (gf) WKV7_BWD(e4m3, float, bf16, float);
+        else WKV7_BWD(e4m3, bf16, bf16, bf16);
+    } else if (x_dt == WKV7_F32) {
+        if (df && gf) WKV7_BWD(float, float, float, float);
+        else if (df) WKV7_BWD(float, float, float, bf16);
+        else if (gf) WKV7_BWD(float, float, bf16, float);
+        else WKV7_BWD(float, float, bf16, bf16);
+    } else {
+        if (df && gf) WKV7_BWD(bf16, bf16, float, float);
+        else if (df) WKV7_BWD(bf16, bf16, float, bf16);
+        else if (gf) WKV7_BWD(bf16, bf16, bf16, float);
+        else WKV7_BWD(bf16, bf16, bf16, bf16);
+    }
+#undef WKV7_BWD
+    sum_parts((long long)B * groups, (long long)cols, partial, sums, stream);
+    conv_params_kernel<<<(unsigned)((cols + 255) / 256), 256, 0, stream>>>(D, W, sums, dweight, dbias);
+    return launch_status();
+}
+
+}  // extern "C"

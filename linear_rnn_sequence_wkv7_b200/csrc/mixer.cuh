@@ -1,0 +1,273 @@
+// Shared pieces of the state-space mixer's kernels (conv.cu, ssm_scan.cu,
+// ssm_bwd.cu, rmsnorm.cu, act8.cu): typed loads and stores, the activation
+// functions, and the 8-bit activation format.
+#pragma once
+
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "wkv7_ssm.h"
+
+namespace wkv7 {
+namespace mixer {
+
+typedef __nv_bfloat16 bf16;
+struct e4m3 { uint8_t code; };       // an 8-bit activation's code (its scale is kept apart)
+
+constexpr int kBlk = WKV7_ACT8_BLOCK;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ---- V consecutive elements ---------------------------------------------------
+
+// Raw words first, values later: a batch of loads is issued before the first
+// conversion waits for one.
+template <typename T, int V> struct Vec {
+    static constexpr int BYTES = V * (int)sizeof(T);
+    uint32_t w[(BYTES + 3) / 4];
+    __device__ __forceinline__ void zero() {
+#pragma unroll
+        for (int i = 0; i < (BYTES + 3) / 4; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (BYTES == 1) w[0] = __ldg(reinterpret_cast<const uint8_t *>(p));
+        else if constexpr (BYTES == 2) w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
+        else if constexpr (BYTES == 4) w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+        else if constexpr (BYTES == 8) {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+            w[0] = u.x, w[1] = u.y;
+        } else {
+#pragma unroll
+            for (int i = 0; i < BYTES / 16; ++i) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&f)[V]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) f[i] = __uint_as_float(w[i]);
+        } else if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                f[i] = __uint_as_float((i & 1) ? (w[i / 2] & 0xffff0000u) : (w[i / 2] << 16));
+        } else if constexpr (V == 1) {
+            f[0] = __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)w[0], __NV_E4M3)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i += 2) {
+                const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+                    (__nv_fp8x2_storage_t)((w[i / 4] >> (8 * (i % 4))) & 0xffffu), __NV_E4M3);
+                const float2 p = __half22float2(__half2(h));
+                f[i] = p.x, f[i + 1] = p.y;
+            }
+        }
+    }
+};
+
+template <int V> __device__ __forceinline__ void storev(float *p, const float (&f)[V]) {
+    if constexpr (V % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < V; i += 4)
+            *reinterpret_cast<float4 *>(p + i) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<float2 *>(p) = make_float2(f[0], f[1]);
+    } else {
+        p[0] = f[0];
+    }
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&t);
+}
+template <int V> __device__ __forceinline__ void storev(bf16 *p, const float (&f)[V]) {
+    if constexpr (V == 8) {
+        *reinterpret_cast<uint4 *>(p) =
+            make_uint4(pack2(f[0], f[1]), pack2(f[2], f[3]), pack2(f[4], f[5]), pack2(f[6], f[7]));
+    } else if constexpr (V == 4) {
+        *reinterpret_cast<uint2 *>(p) = make_uint2(pack2(f[0], f[1]), pack2(f[2], f[3]));
+    } else if constexpr (V == 2) {
+        *reinterpret_cast<uint32_t *>(p) = pack2(f[0], f[1]);
+    } else {
+        p[0] = __float2bfloat16_rn(f[0]);
+    }
+}
+
+// ---- functions ------------------------------------------------------------------
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 1 / (1 + e^-x).  The exponent's rounding, |x| log2(e) 2^-24, is below a bf16
+// result's half step for every |x| < 88; PRECISE (fp32 results) uses expf.
+template <bool PRECISE> __device__ __forceinline__ float sigmoid(float x) {
+    return rcp(1.f + (PRECISE ? expf(-x) : ex2(-x * kLog2e)));
+}
+// log(1 + e^x) = max(x, 0) + log1p(e^-|x|), and log1p(e) = 2 atanh(e / (2 + e)):
+// with e <= 1 the series' argument is at most 1/3, and the terms behind s^15
+// are below 2e-9 of the sum.
+__device__ __forceinline__ float softplus(float x) {
+    const float e = expf(-fabsf(x));
+    const float s = e * rcp(2.f + e), q = s * s;
+    float p = fmaf(q, 1.f / 15, 1.f / 13);
+    p = fmaf(q, p, 1.f / 11);
+    p = fmaf(q, p, 1.f / 9);
+    p = fmaf(q, p, 1.f / 7);
+    p = fmaf(q, p, 1.f / 5);
+    p = fmaf(q, p, 1.f / 3);
+    p = fmaf(q, p, 1.f);
+    return fmaf(2.f * s, p, fmaxf(x, 0.f));
+}
+
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+}
+template <typename F> __device__ __forceinline__ F warp_add(F x) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// ---- roundings ---------------------------------------------------------------------
+
+// The float next to the exact value s + err whose last bit is set (round to
+// odd), or s when err is 0: rounding that to fewer bits gives what rounding the
+// exact value once would.  |err| is at most half a step of s.
+__device__ __forceinline__ float to_odd(float s, float err) {
+    const int b = __float_as_int(s);
+    const bool moves = (err < 0.f || err > 0.f) && !(b & 1);
+    return moves ? __int_as_float(b + (((err > 0.f) == (b >= 0)) ? 1 : -1)) : s;
+}
+// a + b rounded to odd; the error term is the two-sum of Knuth (The Art of
+// Computer Programming, vol. 2, section 4.2.2)
+__device__ __forceinline__ float add_odd(float a, float b) {
+    const float s = a + b, t = s - a;
+    return to_odd(s, (a - (s - t)) + (b - t));
+}
+
+// ---- the 8-bit format --------------------------------------------------------------
+
+// Exponent field of the least power of two >= amax / 448, at least 2^-117:
+// amax = 1.m 2^e and 448 = 1.75 2^8, so 2^(e - 8), or the next above when 1.m > 1.75.
+__device__ __forceinline__ uint32_t act8_exponent(float amax) {
+    const uint32_t b = __float_as_uint(amax);
+    const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u);
+    return (uint32_t)max(e, 10);
+}
+
+// Scale of the warp's block of 128 values, 4 in each lane, and their codes.
+// Infinities and NaN become NaN codes and are left out of amax.
+__device__ __forceinline__ float act8_encode(const float (&x)[4], uint32_t &codes) {
+    float v[4] = {x[0], x[1], x[2], x[3]};
+    float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));   // NaN drops out
+    top = warp_max(top);
+    if (top > 3.4e38f) {                        // uniform in the warp, rare: an infinity may be in the block
+        top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (fabsf(v[i]) <= 3.402823466e38f) top = fmaxf(top, fabsf(v[i]));
+            else v[i] = __uint_as_float(0x7fffffffu);
+        }
+        top = warp_max(top);
+    }
+    const uint32_t e = act8_exponent(top);
+    const float inv = __uint_as_float((254u - e) << 23);
+    if (e == 247u) {            // code 256 would stand for 2^128: the largest numbers take 240, within 2^-4 of them
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (fabsf(v[i] * inv) > 240.f) v[i] = copysignf(240.f, v[i]) * __uint_as_float(e << 23);
+    }
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
+    codes = lo | (hi << 16);
+    return __uint_as_float(e << 23);
+}
+
+// ---- rows cut into blocks of 128 channels, a warp to a block -------------------------
+
+// Channel of a lane's i-th element of block `blk`: four in a row where the row
+// allows vector accesses, else one in every 32.
+template <bool VEC> __device__ __forceinline__ int lane_channel(int blk, int lane, int i) {
+    return blk * kBlk + (VEC ? 4 * lane + i : lane + 32 * i);
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void row_load(const T *row, int blk, int lane, int D, float (&f)[4]) {
+    if constexpr (VEC) {
+        Vec<T, 4> v;
+        v.zero();
+        const int c = lane_channel<true>(blk, lane, 0);
+        if (c < D) v.load(row + c);
+        v.get(f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            Vec<T, 1> v;
+            v.zero();
+            const int c = lane_channel<false>(blk, lane, i);
+            if (c < D) v.load(row + c);
+            float g[1];
+            v.get(g);
+            f[i] = g[0];
+        }
+    }
+}
+template <bool VEC, typename T>
+__device__ __forceinline__ void row_store(T *row, int blk, int lane, int D, const float (&f)[4]) {
+    if constexpr (VEC) {
+        const int c = lane_channel<true>(blk, lane, 0);
+        if (c < D) storev<4>(row + c, f);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = lane_channel<false>(blk, lane, i);
+            const float g[1] = {f[i]};
+            if (c < D) storev<1>(row + c, g);
+        }
+    }
+}
+template <bool VEC>
+__device__ __forceinline__ void row_store_codes(uint8_t *row, int blk, int lane, int D, uint32_t codes) {
+    if constexpr (VEC) {
+        const int c = lane_channel<true>(blk, lane, 0);
+        if (c < D) *reinterpret_cast<uint32_t *>(row + c) = codes;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int c = lane_channel<false>(blk, lane, i);
+            if (c < D) row[c] = (uint8_t)(codes >> (8 * i));
+        }
+    }
+}
+
+// ---- host checks ----------------------------------------------------------------------
+
+inline bool real_dtype(wkv7_dtype d) { return d == WKV7_F32 || d == WKV7_BF16; }
+inline size_t dtype_size(wkv7_dtype d) { return d == WKV7_F32 ? 4 : d == WKV7_BF16 ? 2 : 1; }
+inline bool aligned_to(const void *p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// a pointer to elements of d: present and aligned to its element
+inline bool elem_ok(const void *p, wkv7_dtype d) { return p != nullptr && aligned_to(p, dtype_size(d)); }
+inline bool f32_ok(const void *p) { return p != nullptr && aligned_to(p, 4); }
+inline bool f32_opt(const void *p) { return aligned_to(p, 4); }
+inline int blocks_of(int D) { return (D + kBlk - 1) / kBlk; }
+inline size_t round256(size_t x) { return (x + 255) / 256 * 256; }
+inline wkv7_status launch_status() { return cudaGetLastError() == cudaSuccess ? WKV7_OK : WKV7_ERR_CUDA; }
+inline int sm_count() {
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+    return n;
+}
+constexpr long long kMaxGrid = 2147483647LL;
+constexpr int kMaxTokens = 1 << 30;
+
+}  // namespace mixer
+}  // namespace wkv7
