@@ -1,14 +1,23 @@
 // 8-bit activations by themselves: wkv7_act8_save and wkv7_act8_load.  A warp
-// holds a block of 128 channels, four values a lane, so amax is five shuffles;
-// each warp takes four blocks and issues their loads together.  Bound by memory:
-// 3 bytes a bf16 element.
+// holds a block of 128 channels, four values a lane, and takes eight blocks in a
+// row with their loads issued together.  Bound by memory: 3 bytes a bf16 element.
 #include "mixer.cuh"
 
 namespace wkv7 {
 namespace mixer {
 namespace {
 
-constexpr int kActWarps = 8, kActBatch = 4;
+// (row, block) of consecutive units: one division a warp
+struct Unit {
+    long long row;
+    int blk;
+    __device__ __forceinline__ Unit(long long u, int nblk) : row(u / nblk), blk((int)(u % nblk)) {}
+    __device__ __forceinline__ void next(int nblk) {
+        if (++blk == nblk) blk = 0, ++row;
+    }
+};
+
+constexpr int kActWarps = 8, kActBatch = 8;
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(32 * kActWarps)
@@ -16,20 +25,21 @@ act8_save_kernel(long long units, int nblk, int D, const T *__restrict__ x, long
                  uint8_t *__restrict__ codes, float *__restrict__ scales) {
     const int lane = threadIdx.x & 31;
     const long long first = ((long long)blockIdx.x * kActWarps + (threadIdx.x >> 5)) * kActBatch;
-    float v[kActBatch][4];
+    const Unit start(first, nblk);
+    Row4<T, VEC> v[kActBatch];
+    Unit at = start;
 #pragma unroll
-    for (int m = 0; m < kActBatch; ++m) {
-        const long long u = first + m;
-        if (u < units) row_load<VEC>(x + (u / nblk) * x_ld, (int)(u % nblk), lane, D, v[m]);
-    }
+    for (int m = 0; m < kActBatch; ++m, at.next(nblk)) v[m].load(x + at.row * x_ld, at.blk, lane, first + m < units ? D : 0);
+    at = start;
 #pragma unroll
-    for (int m = 0; m < kActBatch; ++m) {
-        const long long u = first + m;
-        if (u >= units) break;
+    for (int m = 0; m < kActBatch; ++m, at.next(nblk)) {
+        if (first + m >= units) break;
         uint32_t q;
-        const float scale = act8_encode(v[m], q);
-        row_store_codes<VEC>(codes + (u / nblk) * D, (int)(u % nblk), lane, D, q);
-        if (lane == 0) scales[u] = scale;
+        float f[4];
+        v[m].get(f);
+        const float scale = act8_encode(f, q);
+        row_store_codes<VEC>(codes + at.row * D, at.blk, lane, D, q);
+        if (lane == 0) scales[first + m] = scale;
     }
 }
 
@@ -39,22 +49,24 @@ act8_load_kernel(long long units, int nblk, int D, const e4m3 *__restrict__ code
                  const float *__restrict__ scales, T *__restrict__ out) {
     const int lane = threadIdx.x & 31;
     const long long first = ((long long)blockIdx.x * kActWarps + (threadIdx.x >> 5)) * kActBatch;
-    float v[kActBatch][4], s[kActBatch];
+    const Unit start(first, nblk);
+    Row4<e4m3, VEC> v[kActBatch];
+    float s[kActBatch];
+    Unit at = start;
 #pragma unroll
-    for (int m = 0; m < kActBatch; ++m) {
-        const long long u = first + m;
-        if (u < units) {
-            row_load<VEC>(codes + (u / nblk) * D, (int)(u % nblk), lane, D, v[m]);
-            s[m] = __ldg(scales + u);
-        }
+    for (int m = 0; m < kActBatch; ++m, at.next(nblk)) {
+        v[m].load(codes + at.row * D, at.blk, lane, first + m < units ? D : 0);
+        s[m] = first + m < units ? __ldg(scales + first + m) : 0.f;
     }
+    at = start;
 #pragma unroll
-    for (int m = 0; m < kActBatch; ++m) {
-        const long long u = first + m;
-        if (u >= units) break;
+    for (int m = 0; m < kActBatch; ++m, at.next(nblk)) {
+        if (first + m >= units) break;
+        float f[4];
+        v[m].get(f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[m][i] *= s[m];
-        row_store<VEC>(out + (u / nblk) * D, (int)(u % nblk), lane, D, v[m]);
+        for (int i = 0; i < 4; ++i) f[i] *= s[m];
+        row_store<VEC>(out + at.row * D, at.blk, lane, D, f);
     }
 }
 

@@ -21,36 +21,22 @@ namespace {
 
 constexpr int kConvWarps = 4;       // forward: warps a block, each a run of its own
 constexpr int kConvRun = 32;        // tokens a run
-constexpr int kConvAhead = 4;       // tokens whose loads are issued together
+constexpr int kConvAhead = 8;       // tokens whose loads are issued together
 
-// Four channels of one token: raw words, and the scale when they are codes
+// Four channels of one token, and the scale when they are codes
 template <typename T, bool VEC> struct Token {
-    Vec<T, VEC ? 4 : 1> v[VEC ? 1 : 4];
+    Row4<T, VEC> r;
     float scale;
     __device__ __forceinline__ void zero() {
-#pragma unroll
-        for (auto &e : v) e.zero();
+        r.zero();
         scale = 0.f;
     }
     __device__ __forceinline__ void load(const T *row, const float *scales, int blk, int lane, int D) {
-#pragma unroll
-        for (int i = 0; i < (VEC ? 1 : 4); ++i) {
-            v[i].zero();
-            const int c = lane_channel<VEC>(blk, lane, i);
-            if (c < D) v[i].load(row + c);
-        }
+        r.load(row, blk, lane, D);
         if constexpr (sizeof(T) == 1) scale = __ldg(scales);
     }
     __device__ __forceinline__ void get(float (&f)[4]) const {
-        if constexpr (VEC) v[0].get(f);
-        else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float g[1];
-                v[i].get(g);
-                f[i] = g[0];
-            }
-        }
+        r.get(f);
         if constexpr (sizeof(T) == 1) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) f[i] *= scale;
@@ -200,8 +186,9 @@ conv_step_kernel(long long total, int D, const T *__restrict__ x, long long x_bs
     y[id] = from_f32<YT>(silu ? p * sigmoid<sizeof(YT) == 4>(p) : p);
 }
 
-constexpr int kConvBwdWarps = 8;    // backward: runs a block, joined in shared memory
+constexpr int kConvBwdWarps = 4;    // backward: runs a block, joined in shared memory
 constexpr int kConvBwdRun = 64;     // tokens a run
+constexpr int kConvBwdAhead = 4;
 
 struct ConvBwd {
     int B, T, D;
@@ -221,7 +208,7 @@ struct ConvBwd {
 // A warp's run of tokens [t0, t1): at token t it has p_t and dp_t, hence
 // dx_{t-W+1} = sum_j w_j dp_{t-j}; W - 1 tokens behind the run give the rest.
 template <typename T, typename ST, typename DT, typename GT, int W, bool VEC>
-__global__ void __launch_bounds__(32 * kConvBwdWarps)
+__global__ void __launch_bounds__(32 * kConvBwdWarps, VEC ? 3 : 2)
 conv_bwd_kernel(const ConvBwd P) {
     constexpr bool PRECISE = sizeof(GT) == 4;
     __shared__ float part[kConvBwdWarps][W + 1][kBlk];
@@ -261,21 +248,29 @@ conv_bwd_kernel(const ConvBwd P) {
             }
         }
         const int end = t1 + W - 1;
-        for (int tt = t0; tt < end; tt += kConvAhead) {
-            Token<T, VEC> xr[kConvAhead];
-            Token<DT, VEC> gr[kConvAhead];
+        const int last = min(end, P.T);             // tokens behind the sequence count as zero
+        Token<T, VEC> xn[kConvBwdAhead];
+        Token<DT, VEC> gn[kConvBwdAhead];
+        auto fetch = [&](int tt) {
 #pragma unroll
-            for (int k = 0; k < kConvAhead; ++k) {
-                xr[k].zero();
-                gr[k].zero();
-                const int t = tt + k;
-                if (t < end && t < P.T) {
-                    xr[k].load(x + t * P.x_ts, xs + (long long)t * nblk, blk, lane, D);
-                    gr[k].load(dy + (long long)t * D, nullptr, blk, lane, D);
+            for (int k = 0; k < kConvBwdAhead; ++k) {
+                xn[k].zero();
+                gn[k].zero();
+                if (tt + k < last) {
+                    xn[k].load(x + (tt + k) * P.x_ts, xs + (long long)(tt + k) * nblk, blk, lane, D);
+                    gn[k].load(dy + (long long)(tt + k) * D, nullptr, blk, lane, D);
                 }
             }
+        };
+        fetch(t0);
+        for (int tt = t0; tt < end; tt += kConvBwdAhead) {
+            Token<T, VEC> xr[kConvBwdAhead];
+            Token<DT, VEC> gr[kConvBwdAhead];
 #pragma unroll
-            for (int k = 0; k < kConvAhead; ++k) {
+            for (int k = 0; k < kConvBwdAhead; ++k) xr[k] = xn[k], gr[k] = gn[k];
+            if (tt + kConvBwdAhead < end) fetch(tt + kConvBwdAhead);
+#pragma unroll
+            for (int k = 0; k < kConvBwdAhead; ++k) {
                 const int t = tt + k;
                 if (t >= end) break;
                 float v[4], g[4], o[4];

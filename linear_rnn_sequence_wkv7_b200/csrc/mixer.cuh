@@ -110,27 +110,41 @@ __device__ __forceinline__ float rcp(float x) {
 template <bool PRECISE> __device__ __forceinline__ float sigmoid(float x) {
     return rcp(1.f + (PRECISE ? expf(-x) : ex2(-x * kLog2e)));
 }
-// log(1 + e^x) = max(x, 0) + log1p(e^-|x|), and log1p(e) = 2 atanh(e / (2 + e)):
-// with e <= 1 the series' argument is at most 1/3, and the terms behind s^15
-// are below 2e-9 of the sum.
-__device__ __forceinline__ float softplus(float x) {
-    const float e = expf(-fabsf(x));
-    const float s = e * rcp(2.f + e), q = s * s;
-    float p = fmaf(q, 1.f / 15, 1.f / 13);
-    p = fmaf(q, p, 1.f / 11);
-    p = fmaf(q, p, 1.f / 9);
-    p = fmaf(q, p, 1.f / 7);
-    p = fmaf(q, p, 1.f / 5);
-    p = fmaf(q, p, 1.f / 3);
-    p = fmaf(q, p, 1.f);
-    return fmaf(2.f * s, p, fmaxf(x, 0.f));
+// log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in (0, 1]; log1p(e) / e by its
+// Chebyshev interpolant of degree 9 on [0, 1] (off by 6e-9 of the value, 1e-7
+// evaluated in fp32), which keeps small values exact where log(1 + e) would not.
+// Not PRECISE (bf16 inputs, which are off by 2^-9 themselves): e by one ex2, off
+// by |x| log2(e) 2^-24.  Two values at a time: one packed instruction a step.
+template <bool PRECISE> __device__ __forceinline__ float2 softplus2(float2 x) {
+    float2 e;
+    if constexpr (PRECISE) {
+        e = make_float2(expf(-fabsf(x.x)), expf(-fabsf(x.y)));
+    } else {
+        const float2 t = __fmul2_rn(make_float2(fabsf(x.x), fabsf(x.y)), make_float2(-kLog2e, -kLog2e));
+        e = make_float2(ex2(t.x), ex2(t.y));
+    }
+    constexpr float c[10] = {-3.1760570e-3f, 1.9542528e-2f, -5.6373615e-2f, 1.0543624e-1f, -1.5269667e-1f,
+                             1.9663274e-1f,  -2.4951616e-1f, 3.3329710e-1f, -4.9999893e-1f, 1.f};
+    float2 p = make_float2(c[0], c[0]);
+#pragma unroll
+    for (int i = 1; i < 10; ++i) p = __ffma2_rn(p, e, make_float2(c[i], c[i]));
+    return __ffma2_rn(e, p, make_float2(fmaxf(x.x, 0.f), fmaxf(x.y, 0.f)));
+}
+template <bool PRECISE> __device__ __forceinline__ float softplus(float x) {
+    return softplus2<PRECISE>(make_float2(x, x)).x;
+}
+// softplus of V values in place
+template <bool PRECISE, int V> __device__ __forceinline__ void softplus_all(float (&x)[V]) {
+    if constexpr (V == 1) x[0] = softplus<PRECISE>(x[0]);
+    else {
+#pragma unroll
+        for (int i = 0; i < V; i += 2) {
+            const float2 r = softplus2<PRECISE>(make_float2(x[i], x[i + 1]));
+            x[i] = r.x, x[i + 1] = r.y;
+        }
+    }
 }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    return x;
-}
 template <typename F> __device__ __forceinline__ F warp_add(F x) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
@@ -147,49 +161,78 @@ __device__ __forceinline__ float to_odd(float s, float err) {
     const bool moves = (err < 0.f || err > 0.f) && !(b & 1);
     return moves ? __int_as_float(b + (((err > 0.f) == (b >= 0)) ? 1 : -1)) : s;
 }
-// a + b rounded to odd; the error term is the two-sum of Knuth (The Art of
-// Computer Programming, vol. 2, section 4.2.2)
-__device__ __forceinline__ float add_odd(float a, float b) {
-    const float s = a + b, t = s - a;
-    return to_odd(s, (a - (s - t)) + (b - t));
+// (a + b) - fl(a + b), exactly: the two-sum of Knuth (The Art of Computer
+// Programming, vol. 2, section 4.2.2); s = fl(a + b)
+__device__ __forceinline__ float sum_error(float a, float b, float s) {
+    const float t = s - a;
+    return (a - (s - t)) + (b - t);
 }
 
 // ---- the 8-bit format --------------------------------------------------------------
 
 // Exponent field of the least power of two >= amax / 448, at least 2^-117:
 // amax = 1.m 2^e and 448 = 1.75 2^8, so 2^(e - 8), or the next above when 1.m > 1.75.
-__device__ __forceinline__ uint32_t act8_exponent(float amax) {
-    const uint32_t b = __float_as_uint(amax);
+__device__ __forceinline__ uint32_t act8_exponent(uint32_t b) {     // b: amax's bits
     const int e = (int)(b >> 23) - 8 + ((b & 0x7fffffu) > 0x600000u);
     return (uint32_t)max(e, 10);
 }
 
-// Scale of the warp's block of 128 values, 4 in each lane, and their codes.
-// Infinities and NaN become NaN codes and are left out of amax.
+// The warp's block of 128 values, 4 in each lane.  Bits of absolute values order
+// like the values, so amax is one warp-wide integer maximum.
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t act8_top(const float (&v)[4]) {
+    const uint32_t m = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
+    return __reduce_max_sync(0xffffffffu, m);
+}
+__device__ __forceinline__ uint32_t act8_pack(const float (&q)[4]) {
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(q[2], q[3]), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
+}
+// Scale and codes.  Infinities and NaN become NaN codes and are left out of amax.
 __device__ __forceinline__ float act8_encode(const float (&x)[4], uint32_t &codes) {
     float v[4] = {x[0], x[1], x[2], x[3]};
-    float top = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));   // NaN drops out
-    top = warp_max(top);
-    if (top > 3.4e38f) {                        // uniform in the warp, rare: an infinity may be in the block
-        top = 0.f;
+    uint32_t top = act8_top(v);
+    if (top >= 0x7f800000u) {                   // uniform in the warp, rare
+        top = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (fabsf(v[i]) <= 3.402823466e38f) top = fmaxf(top, fabsf(v[i]));
+            if (abs_bits(v[i]) < 0x7f800000u) top = max(top, abs_bits(v[i]));
             else v[i] = __uint_as_float(0x7fffffffu);
         }
-        top = warp_max(top);
+        top = __reduce_max_sync(0xffffffffu, top);
     }
     const uint32_t e = act8_exponent(top);
     const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] *= inv;
     if (e == 247u) {            // code 256 would stand for 2^128: the largest numbers take 240, within 2^-4 of them
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            if (fabsf(v[i] * inv) > 240.f) v[i] = copysignf(240.f, v[i]) * __uint_as_float(e << 23);
+            if (fabsf(v[i]) > 240.f) v[i] = copysignf(240.f, v[i]);
     }
-    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[0] * inv, v[1] * inv), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[2] * inv, v[3] * inv), __NV_SATFINITE, __NV_E4M3);
-    codes = lo | (hi << 16);
+    codes = act8_pack(v);
     return __uint_as_float(e << 23);
+}
+// The same where every value is known to within 2^-21 of itself only: false if a
+// code or the scale could depend on more (a scaled value next to the middle
+// between two codes or among the codes' subnormals, amax next to a power's
+// border, numbers too large).  Uniform in the warp.
+__device__ __forceinline__ bool act8_encode_sure(const float (&x)[4], uint32_t &codes, float &scale) {
+    const uint32_t top = act8_top(x), e = act8_exponent(top);
+    const float inv = __uint_as_float((254u - e) << 23);
+    bool close = (top & 0x7fffffu) - 0x5ffff8u <= 16u || top > 0x7b000000u || top < 0x08000000u;
+    float q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        q[i] = x[i] * inv;
+        const uint32_t b = __float_as_uint(q[i]);
+        // the middle between two codes: the leading bit behind the three that are kept, alone
+        close |= (b & 0xfffffu) - 0x7fff8u <= 16u || (fabsf(q[i]) < 0.015625f && q[i] != 0.f);
+    }
+    codes = act8_pack(q);
+    scale = __uint_as_float(e << 23);
+    return !__any_sync(0xffffffffu, close);
 }
 
 // ---- rows cut into blocks of 128 channels, a warp to a block -------------------------
@@ -199,26 +242,38 @@ __device__ __forceinline__ float act8_encode(const float (&x)[4], uint32_t &code
 template <bool VEC> __device__ __forceinline__ int lane_channel(int blk, int lane, int i) {
     return blk * kBlk + (VEC ? 4 * lane + i : lane + 32 * i);
 }
-template <bool VEC, typename T>
-__device__ __forceinline__ void row_load(const T *row, int blk, int lane, int D, float (&f)[4]) {
-    if constexpr (VEC) {
-        Vec<T, 4> v;
-        v.zero();
-        const int c = lane_channel<true>(blk, lane, 0);
-        if (c < D) v.load(row + c);
-        v.get(f);
-    } else {
+// A lane's four elements of a block: raw words first, values later
+template <typename T, bool VEC> struct Row4 {
+    Vec<T, VEC ? 4 : 1> v[VEC ? 1 : 4];
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            Vec<T, 1> v;
-            v.zero();
-            const int c = lane_channel<false>(blk, lane, i);
-            if (c < D) v.load(row + c);
-            float g[1];
-            v.get(g);
-            f[i] = g[0];
+        for (auto &e : v) e.zero();
+    }
+    __device__ __forceinline__ void load(const T *row, int blk, int lane, int D) {
+#pragma unroll
+        for (int i = 0; i < (VEC ? 1 : 4); ++i) {
+            v[i].zero();
+            const int c = lane_channel<VEC>(blk, lane, i);
+            if (c < D) v[i].load(row + c);
         }
     }
+    __device__ __forceinline__ void get(float (&f)[4]) const {
+        if constexpr (VEC) v[0].get(f);
+        else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float g[1];
+                v[i].get(g);
+                f[i] = g[0];
+            }
+        }
+    }
+};
+template <bool VEC, typename T>
+__device__ __forceinline__ void row_load(const T *row, int blk, int lane, int D, float (&f)[4]) {
+    Row4<T, VEC> r;
+    r.load(row, blk, lane, D);
+    r.get(f);
 }
 template <bool VEC, typename T>
 __device__ __forceinline__ void row_store(T *row, int blk, int lane, int D, const float (&f)[4]) {

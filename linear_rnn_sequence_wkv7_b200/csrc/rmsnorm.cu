@@ -11,34 +11,88 @@
 //
 // The 8-bit output rounds to 4 significant bits, and a value next to a border
 // between two codes would fall on either side by fp32's rounding; the row's sum
-// is therefore carried in fp64 from every four elements on, and y in two floats
-// (value and error), rounded once.
+// is therefore carried in fp64 from every four elements on, and where a block has
+// a y next to a border (one block in a thousand) y is taken in two floats (value
+// and error) and rounded once.
 #include "mixer.cuh"
 
 namespace wkv7 {
 namespace mixer {
 namespace {
 
-constexpr int kNormMaxWarps = 16;
+constexpr int kNormMaxWarps = 32;
 
-// MB blocks of a row by run-time type: one branch around the whole batch of loads
-template <bool VEC, int MB>
-__device__ __forceinline__ void batch_load(const void *p, wkv7_dtype dt, long long off, int blk0, int step, int nblk,
-                                           int lane, int D, float (&f)[MB][4]) {
-    if (dt == WKV7_BF16) {
-        const bf16 *row = static_cast<const bf16 *>(p) + off;
-#pragma unroll
-        for (int m = 0; m < MB; ++m) row_load<VEC>(row, blk0 + m * step, lane, D, f[m]);
-    } else if (dt == WKV7_F32) {
-        const float *row = static_cast<const float *>(p) + off;
-#pragma unroll
-        for (int m = 0; m < MB; ++m) row_load<VEC>(row, blk0 + m * step, lane, D, f[m]);
-    } else {
-        const e4m3 *row = static_cast<const e4m3 *>(p) + off;
-#pragma unroll
-        for (int m = 0; m < MB; ++m) row_load<VEC>(row, blk0 + m * step, lane, D, f[m]);
-    }
+// E: whether 8-bit codes can be among the types; WIDE: whether fp32 can
+template <bool WIDE, bool E, typename F> __device__ __forceinline__ void by_dtype(wkv7_dtype dt, F &&f) {
+    if (E && dt == WKV7_E4M3) f(e4m3());
+    else if (!WIDE || dt == WKV7_BF16) f(bf16());
+    else if constexpr (WIDE) f(float());
 }
+// MB blocks of a row, one branch around the batch
+template <bool VEC, int MB, bool WIDE, bool E>
+__device__ __forceinline__ void batch_load(const void *p, wkv7_dtype dt, long long off, int blk0, int step, int lane,
+                                           int D, float (&f)[MB][4]) {
+    by_dtype<WIDE, E>(dt, [&](auto t) {
+        const decltype(t) *row = static_cast<const decltype(t) *>(p) + off;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) row_load<VEC>(row, blk0 + m * step, lane, D, f[m]);
+    });
+}
+
+// Rows on their way: kAhead rows of each tensor, copied to shared memory
+// (cp.async) by the thread that reads them, so no barrier is needed.  A slot is
+// four values, 8 bytes or (WIDE) 16; slots behind the row's end stay zero.
+constexpr int kAhead = 4;
+template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
+}
+template <int MB, bool WIDE, int TENSORS> struct Ring {
+    static constexpr int SLOT = WIDE ? 16 : 8;
+    unsigned char *base;
+    __device__ __forceinline__ unsigned char *slot(int stage, int tensor, int m) const {
+        return base + ((size_t)((stage * TENSORS + tensor) * MB + m) * blockDim.x + threadIdx.x) * SLOT;
+    }
+    __device__ __forceinline__ void clear() const {
+        for (int i = 0; i < kAhead * TENSORS * MB; ++i)
+            for (int k = 0; k < SLOT; k += 8) *reinterpret_cast<uint2 *>(slot(0, 0, i) + k) = make_uint2(0, 0);
+    }
+    template <bool E>
+    __device__ __forceinline__ void fetch(int stage, int tensor, const void *p, wkv7_dtype dt, long long off, int blk0,
+                                          int step, int lane, int D) const {
+        by_dtype<WIDE, E>(dt, [&](auto t) {
+            const decltype(t) *row = static_cast<const decltype(t) *>(p) + off;
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                const int c = lane_channel<true>(blk0 + m * step, lane, 0);
+                if (c < D) copy_async<4 * (int)sizeof(t)>(smem_u32(slot(stage, tensor, m)), row + c);
+            }
+        });
+    }
+    template <bool E>
+    __device__ __forceinline__ void get(int stage, int tensor, wkv7_dtype dt, float (&f)[MB][4]) const {
+        by_dtype<WIDE, E>(dt, [&](auto t) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                Vec<decltype(t), 4> v;
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(slot(stage, tensor, m));
+                if constexpr (sizeof(v.w) == 16) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(w);
+                    v.w[0] = q.x, v.w[1] = q.y, v.w[2] = q.z, v.w[3] = q.w;
+                } else if constexpr (sizeof(v.w) == 8) {
+                    const uint2 q = *reinterpret_cast<const uint2 *>(w);
+                    v.w[0] = q.x, v.w[1] = q.y;
+                } else {
+                    v.w[0] = w[0];
+                }
+                v.get(f[m]);
+            }
+        });
+    }
+};
+template <int MB, bool WIDE> constexpr size_t ring_bytes(int tensors, int threads) {
+    return (size_t)kAhead * tensors * MB * threads * (WIDE ? 16 : 8);
+}
+
 template <bool VEC, int MB>
 __device__ __forceinline__ void batch_store(void *p, wkv7_dtype dt, long long off, int blk0, int step, int lane,
                                             int D, const float (&f)[MB][4]) {
@@ -64,87 +118,143 @@ template <typename F> __device__ __forceinline__ F block_add(F x, F *shared, int
     return t;
 }
 
+// blocks of 128 a warp holds, and the threads of a row's block at most
+__host__ __device__ constexpr int norm_max_threads(int MB) { return MB == 1 ? 256 : MB == 2 ? 512 : 1024; }
+
 struct NormFwd {
+    long long rows;
     int D;
     wkv7_dtype x_dt, r_dt, y_dt;
     const void *x;
     long long x_ld;
     const void *residual;
     const float *weight;
-    float eps;
+    double eps, inv_D;
     void *residual_out, *y;
     float *y_scales;
     uint8_t *s_codes;
     float *s_scales, *rstd;
 };
 
-template <bool VEC, int MB>
-__global__ void __launch_bounds__(32 * kNormMaxWarps)
+// A block takes rows blockIdx.x, + gridDim.x, ...  MB <= 2 with vector accesses:
+// the next rows are on their way and the weight stays in registers.
+template <bool VEC, int MB, bool WIDE>
+__global__ void __launch_bounds__(norm_max_threads(MB), 1024 / norm_max_threads(MB))
 rmsnorm_fwd_kernel(const NormFwd P) {
-    __shared__ double shared[kNormMaxWarps];
-    const long long row = blockIdx.x;
+    constexpr bool RING = VEC && MB <= 2, KEEP = MB <= 2;
+    __shared__ double shared[2][kNormMaxWarps];
+    extern __shared__ __align__(16) unsigned char ring_mem[];
+    const Ring<MB, WIDE, 2> ring{ring_mem};
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int nblk = (P.D + kBlk - 1) / kBlk, D = P.D;
-    float s[MB][4], o[MB][4];       // the sum to nearest, and rounded to odd for what keeps fewer bits
-    batch_load<VEC, MB>(P.x, P.x_dt, row * P.x_ld, warp, warps, nblk, lane, D, s);
-    if (P.residual) batch_load<VEC, MB>(P.residual, P.r_dt, row * D, warp, warps, nblk, lane, D, o);
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float a = s[m][i], b = P.residual ? o[m][i] : 0.f;
-            o[m][i] = add_odd(a, b);
-            s[m][i] = a + b;
+    float w[MB][4];
+    auto fetch = [&](long long row, int stage) {
+        if (row < P.rows) {
+            ring.template fetch<false>(stage, 0, P.x, P.x_dt, row * P.x_ld, warp, warps, lane, D);
+            if (P.residual) ring.template fetch<false>(stage, 1, P.residual, P.r_dt, row * D, warp, warps, lane, D);
         }
-    double sum = 0;
+        cp_async_commit();
+    };
+    if constexpr (RING) {
+        ring.clear();
 #pragma unroll
-    for (int m = 0; m < MB; ++m)
-        sum += (double)fmaf(s[m][0], s[m][0], fmaf(s[m][1], s[m][1], fmaf(s[m][2], s[m][2], s[m][3] * s[m][3])));
-    if (P.residual_out) {
-        if (P.r_dt == WKV7_BF16) batch_store<VEC, MB>(P.residual_out, WKV7_BF16, row * D, warp, warps, lane, D, o);
-        else batch_store<VEC, MB>(P.residual_out, WKV7_F32, row * D, warp, warps, lane, D, s);
+        for (int i = 0; i < kAhead - 1; ++i) fetch(blockIdx.x + (long long)i * gridDim.x, i);
     }
-    if (P.s_codes) {
+    if (KEEP) {
+#pragma unroll
+        for (int m = 0; m < MB; ++m) row_load<VEC>(P.weight, warp + m * warps, lane, D, w[m]);
+    }
+    int turn = 0, stage = 0;
+    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x, turn ^= 1, stage = (stage + 1) % kAhead) {
+        float s[MB][4], o[MB][4];   // the sum to nearest, and rounded to odd for what keeps fewer bits
+        if constexpr (RING) {
+            fetch(row + (kAhead - 1ll) * gridDim.x, (stage + kAhead - 1) % kAhead);
+            cp_async_wait<kAhead - 1>();
+            ring.template get<false>(stage, 0, P.x_dt, s);
+            if (P.residual) ring.template get<false>(stage, 1, P.r_dt, o);
+        } else {
+            batch_load<VEC, MB, WIDE, false>(P.x, P.x_dt, row * P.x_ld, warp, warps, lane, D, s);
+            if (P.residual) batch_load<VEC, MB, WIDE, false>(P.residual, P.r_dt, row * D, warp, warps, lane, D, o);
+        }
+        double sum = 0;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            if (P.residual) {
+                float err[4];
+                bool exact = true;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float a = s[m][i], b = o[m][i];
+                    s[m][i] = a + b;
+                    err[i] = sum_error(a, b, s[m][i]);
+                    exact &= err[i] == 0.f;
+                    o[m][i] = s[m][i];
+                }
+                if (!exact) {           // of two bf16 numbers: only where they are 2^16 apart
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[m][i] = to_odd(s[m][i], err[i]);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[m][i] = s[m][i];
+            }
+            sum += (double)fmaf(s[m][0], s[m][0], fmaf(s[m][1], s[m][1], fmaf(s[m][2], s[m][2], s[m][3] * s[m][3])));
+        }
+        if (P.residual_out) {
+            if (P.r_dt == WKV7_BF16) batch_store<VEC, MB>(P.residual_out, WKV7_BF16, row * D, warp, warps, lane, D, o);
+            else batch_store<VEC, MB>(P.residual_out, WKV7_F32, row * D, warp, warps, lane, D, s);
+        }
+        if (P.s_codes) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                const int blk = warp + m * warps;
+                if (blk >= nblk) break;
+                uint32_t q;
+                const float scale = act8_encode(o[m], q);
+                row_store_codes<VEC>(P.s_codes + row * D, blk, lane, D, q);
+                if (lane == 0) P.s_scales[row * nblk + blk] = scale;
+            }
+        }
+        // two buffers in turn: a warp that is a row ahead does not overwrite sums still being read
+        sum = block_add(sum, shared[turn], warp, warps);
+        // 1 / sqrt in fp32, and one Newton step in fp64
+        const double mean = fma(sum, P.inv_D, P.eps), r0 = (double)rsqrtf((float)mean);
+        const double inv = isinf(r0) ? r0 : fma(0.5 * r0, fma(-mean * r0, r0, 1.0), r0);
+        const float ih = (float)inv, il = isinf(r0) ? 0.f : (float)(inv - (double)ih);
+        if (P.rstd && threadIdx.x == 0) P.rstd[row] = ih;
+        if (!KEEP) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m) row_load<VEC>(P.weight, warp + m * warps, lane, D, w[m]);
+        }
+        if (P.y_dt != WKV7_E4M3) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[m][i] = s[m][i] * ih * w[m][i];
+            batch_store<VEC, MB>(P.y, P.y_dt, row * D, warp, warps, lane, D, s);
+            continue;
+        }
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             const int blk = warp + m * warps;
             if (blk >= nblk) break;
+            float v[4], scale;
             uint32_t q;
-            const float scale = act8_encode(o[m], q);
-            row_store_codes<VEC>(P.s_codes + row * D, blk, lane, D, q);
-            if (lane == 0) P.s_scales[row * nblk + blk] = scale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = s[m][i] * w[m][i] * ih;      // off by 3 half steps at most
+            if (!act8_encode_sure(v, q, scale)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = s[m][i] * w[m][i], pl = fmaf(s[m][i], w[m][i], -p);
+                    const float y = p * ih, yl = fmaf(p, ih, -y) + fmaf(pl, ih, p * il);
+                    const float top = y + yl;
+                    v[i] = to_odd(top, yl - (top - y));
+                }
+                scale = act8_encode(v, q);
+            }
+            row_store_codes<VEC>(static_cast<uint8_t *>(P.y) + row * D, blk, lane, D, q);
+            if (lane == 0) P.y_scales[row * nblk + blk] = scale;
         }
-    }
-    sum = block_add(sum, shared, warp, warps);
-    const double inv = 1.0 / sqrt(sum / D + (double)P.eps);
-    const float ih = (float)inv, il = (float)(inv - (double)ih);
-    if (P.rstd && threadIdx.x == 0) P.rstd[row] = ih;
-    float w[MB][4];
-    batch_load<VEC, MB>(P.weight, WKV7_F32, 0, warp, warps, nblk, lane, D, w);
-    if (P.y_dt != WKV7_E4M3) {
-#pragma unroll
-        for (int m = 0; m < MB; ++m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[m][i] = s[m][i] * ih * w[m][i];
-        batch_store<VEC, MB>(P.y, P.y_dt, row * D, warp, warps, lane, D, s);
-        return;
-    }
-#pragma unroll
-    for (int m = 0; m < MB; ++m) {
-        const int blk = warp + m * warps;
-        if (blk >= nblk) break;
-        float v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float p = s[m][i] * w[m][i], pl = fmaf(s[m][i], w[m][i], -p);
-            const float y = p * ih, yl = fmaf(p, ih, -y) + fmaf(pl, ih, p * il);
-            const float top = y + yl;
-            v[i] = to_odd(top, yl - (top - y));
-        }
-        uint32_t q;
-        const float scale = act8_encode(v, q);
-        row_store_codes<VEC>(static_cast<uint8_t *>(P.y) + row * D, blk, lane, D, q);
-        if (lane == 0) P.y_scales[row * nblk + blk] = scale;
     }
 }
 
@@ -157,69 +267,136 @@ struct NormBwd {
     const void *dy, *dres;
     void *dx;
     float *partial;          // [grid][D]
+    float inv_D;
 };
 
-// A block takes rows blockIdx.x, + gridDim.x, ...; its share of dw stays in
-// registers and goes to partial[blockIdx.x].
-template <bool VEC, int MB>
-__global__ void __launch_bounds__(32 * kNormMaxWarps)
+// The same walk over rows; a block's share of dw goes to partial[blockIdx.x].
+// KEEP: w and dw stay in registers (dw in shared memory otherwise).
+template <bool VEC, int MB, bool WIDE>
+__global__ void __launch_bounds__(norm_max_threads(MB), 1024 / norm_max_threads(MB))
 rmsnorm_bwd_kernel(const NormBwd P) {
+    constexpr bool RING = VEC && MB <= 2, KEEP = MB <= 2;
     __shared__ float shared[2][kNormMaxWarps];
+    extern __shared__ __align__(16) unsigned char ring_mem[];
+    const Ring<MB, WIDE, 3> ring{ring_mem};
+    float *s_dw = reinterpret_cast<float *>(ring_mem);      // [4 MB][threads] when not KEEP
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int nblk = (P.D + kBlk - 1) / kBlk, D = P.D;
     float w[MB][4], dw[MB][4];
-    batch_load<VEC, MB>(P.weight, WKV7_F32, 0, warp, warps, nblk, lane, D, w);
-#pragma unroll
-    for (int m = 0; m < MB; ++m)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dw[m][i] = 0.f;
-    int turn = 0;
-    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x, turn ^= 1) {
-        float s[MB][4], g[MB][4], d[MB][4], scale[MB];
-        batch_load<VEC, MB>(P.s, P.s_dt, row * D, warp, warps, nblk, lane, D, s);
-        batch_load<VEC, MB>(P.dy, P.dy_dt, row * D, warp, warps, nblk, lane, D, g);
-        if (P.dres) batch_load<VEC, MB>(P.dres, P.g_dt, row * D, warp, warps, nblk, lane, D, d);
-        const float rs = __ldg(P.rstd + row);
+    float next_r = 0.f, next_scale[MB];
+    auto fetch = [&](long long row, int stage) {
+        if (row < P.rows) {
+            ring.template fetch<true>(stage, 0, P.s, P.s_dt, row * D, warp, warps, lane, D);
+            ring.template fetch<false>(stage, 1, P.dy, P.dy_dt, row * D, warp, warps, lane, D);
+            if (P.dres) ring.template fetch<false>(stage, 2, P.dres, P.g_dt, row * D, warp, warps, lane, D);
+        }
+        cp_async_commit();
+    };
+    auto fetch_small = [&](long long row) {
+        if (row >= P.rows) return;
+        next_r = __ldg(P.rstd + row);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             const int blk = warp + m * warps;
-            scale[m] = (P.s_dt == WKV7_E4M3 && blk < nblk) ? __ldg(P.s_scales + row * nblk + blk) : 1.f;
+            next_scale[m] = (P.s_dt == WKV7_E4M3 && blk < nblk) ? __ldg(P.s_scales + row * nblk + blk) : 1.f;
         }
+    };
+    if constexpr (RING) {
+        ring.clear();
+#pragma unroll
+        for (int i = 0; i < kAhead - 1; ++i) fetch(blockIdx.x + (long long)i * gridDim.x, i);
+    }
+    fetch_small(blockIdx.x);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) {
+        if (KEEP) row_load<VEC>(P.weight, warp + m * warps, lane, D, w[m]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (KEEP) dw[m][i] = 0.f;
+            else s_dw[(4 * m + i) * blockDim.x + threadIdx.x] = 0.f;
+        }
+    }
+    int turn = 0, stage = 0;
+    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x, turn ^= 1, stage = (stage + 1) % kAhead) {
+        float s[MB][4], g[MB][4];
+        if constexpr (RING) {
+            fetch(row + (kAhead - 1ll) * gridDim.x, (stage + kAhead - 1) % kAhead);
+            cp_async_wait<kAhead - 1>();
+            ring.template get<true>(stage, 0, P.s_dt, s);
+            ring.template get<false>(stage, 1, P.dy_dt, g);
+        } else {
+            batch_load<VEC, MB, WIDE, true>(P.s, P.s_dt, row * D, warp, warps, lane, D, s);
+            batch_load<VEC, MB, WIDE, false>(P.dy, P.dy_dt, row * D, warp, warps, lane, D, g);
+        }
+        const float r = next_r;
         float c = 0.f;
 #pragma unroll
-        for (int m = 0; m < MB; ++m)
+        for (int m = 0; m < MB; ++m) {
+            const float q = next_scale[m] * r;
+            if (!KEEP) row_load<VEC>(P.weight, warp + m * warps, lane, D, w[m]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float xh = s[m][i] * scale[m] * rs;
-                dw[m][i] = fmaf(g[m][i], xh, dw[m][i]);
+                const float xh = s[m][i] * q;
+                if (KEEP) dw[m][i] = fmaf(g[m][i], xh, dw[m][i]);
+                else s_dw[(4 * m + i) * blockDim.x + threadIdx.x] += g[m][i] * xh;
                 s[m][i] = xh;
                 g[m][i] *= w[m][i];
                 c = fmaf(g[m][i], xh, c);
             }
-        // two buffers in turn: a warp that is a row ahead does not overwrite sums still being read
-        c = block_add(c, shared[turn], warp, warps) / (float)D;
+        }
+        fetch_small(row + gridDim.x);
+        c = block_add(c, shared[turn], warp, warps) * P.inv_D;
 #pragma unroll
         for (int m = 0; m < MB; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float v = rs * fmaf(-c, s[m][i], g[m][i]);
-                s[m][i] = P.dres ? d[m][i] + v : v;
-            }
+            for (int i = 0; i < 4; ++i) s[m][i] = r * fmaf(-c, s[m][i], g[m][i]);
+        if (P.dres) {
+            if constexpr (RING) ring.template get<false>(stage, 2, P.g_dt, g);
+            else batch_load<VEC, MB, WIDE, false>(P.dres, P.g_dt, row * D, warp, warps, lane, D, g);
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[m][i] += g[m][i];
+        }
         batch_store<VEC, MB>(P.dx, P.g_dt, row * D, warp, warps, lane, D, s);
+    }
+    if (!KEEP) {
+#pragma unroll
+        for (int m = 0; m < MB; ++m)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dw[m][i] = s_dw[(4 * m + i) * blockDim.x + threadIdx.x];
     }
     batch_store<VEC, MB>(P.partial, WKV7_F32, (long long)blockIdx.x * D, warp, warps, lane, D, dw);
 }
 
-int norm_batch(int nblk) { return nblk <= 8 ? 1 : nblk <= 16 ? 2 : nblk <= 32 ? 4 : 8; }
+int norm_batch(int nblk) { return nblk <= 8 ? 1 : nblk <= 32 ? 2 : 4; }
 
-long long norm_bwd_grid(long long rows, int D) {
-    const int sms = sm_count(), nblk = blocks_of(D), mb = norm_batch(nblk);
+int norm_threads(int nblk) { return 32 * ((nblk + norm_batch(nblk) - 1) / norm_batch(nblk)); }
+
+// Blocks that walk the rows: as many as the SMs hold with `per_sm` threads each
+long long norm_grid(long long rows, int D, int per_sm) {
+    const int sms = sm_count(), threads = norm_threads(blocks_of(D));
     if (sms <= 0) return 0;
-    const int threads = 32 * ((nblk + mb - 1) / mb);
-    // as many rows in flight as the SMs hold at about 100 registers a thread
-    const long long most = (long long)sms * (640 / threads > 0 ? 640 / threads : 1);
+    const long long most = (long long)sms * (per_sm / threads > 0 ? per_sm / threads : 1);
     return rows < most ? rows : most;
 }
+constexpr int kNormThreads = 1024;      // on an SM, at 64 registers a thread
+
+template <typename K, typename P>
+wkv7_status norm_launch(K kernel, const P &p, long long grid, int threads, size_t smem, cudaStream_t st) {
+    if (smem > 40 * 1024 &&         // 48 KiB with the kernel's own arrays need no leave
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return WKV7_ERR_CUDA;
+    kernel<<<(unsigned)grid, threads, smem, st>>>(p);
+    return launch_status();
+}
+// blocks of 128 a warp as a template argument
+#define WKV7_NORM_MB(V, R)                    \
+    do {                                      \
+        if (mb == 1) WKV7_NORM(V, 1, R);      \
+        else if (mb == 2) WKV7_NORM(V, 2, R); \
+        else WKV7_NORM(V, 4, R);              \
+    } while (0)
 
 wkv7_status norm_dims(long long rows, int D) {
     if (rows < 0 || D < 0) return WKV7_ERR_INVALID_ARG;
@@ -276,27 +453,29 @@ wkv7_status wkv7_rmsnorm_forward(long long rows, int D, wkv7_dtype x_dt, wkv7_dt
         return WKV7_ERR_INVALID_ARG;
     if ((y_dt == WKV7_E4M3) != (y_scales != nullptr) || !f32_opt(y_scales)) return WKV7_ERR_INVALID_ARG;
     if ((s_codes != nullptr) != (s_scales != nullptr) || !f32_opt(s_scales)) return WKV7_ERR_INVALID_ARG;
-    const NormFwd P{D, x_dt, r_dt, y_dt, x, x_ld, residual, weight, eps, residual_out, y, y_scales,
-                    (uint8_t *)s_codes, s_scales, rstd};
+    const NormFwd P{rows, D, x_dt, r_dt, y_dt, x, x_ld, residual, weight, (double)eps, 1.0 / D, residual_out, y,
+                    y_scales, (uint8_t *)s_codes, s_scales, rstd};
+    const long long grid = norm_grid(rows, D, kNormThreads);
+    if (grid <= 0) return WKV7_ERR_CUDA;
     const bool vec = D % 4 == 0 && x_ld % 4 == 0 && aligned_to(x, 4 * dtype_size(x_dt)) &&
                      aligned_to(residual, 4 * dtype_size(r_dt)) && aligned_to(residual_out, 4 * dtype_size(r_dt)) &&
                      aligned_to(y, 4 * dtype_size(y_dt)) && aligned_to(weight, 16) && aligned_to(s_codes, 4);
-    const int nblk = blocks_of(D), mb = norm_batch(nblk), threads = 32 * ((nblk + mb - 1) / mb);
-#define WKV7_NORM(V, M) rmsnorm_fwd_kernel<V, M><<<(unsigned)rows, threads, 0, stream>>>(P)
-#define WKV7_NORM_MB(V)                                                                                   \
-    (mb == 1 ? (void)(WKV7_NORM(V, 1)) : mb == 2 ? (void)(WKV7_NORM(V, 2)) : mb == 4 ? (void)(WKV7_NORM(V, 4)) \
-                                                                            : (void)(WKV7_NORM(V, 8)))
-    if (vec) WKV7_NORM_MB(true);
-    else WKV7_NORM_MB(false);
-#undef WKV7_NORM_MB
+    const int mb = norm_batch(blocks_of(D)), threads = norm_threads(blocks_of(D));
+    const bool narrow = x_dt == WKV7_BF16 && (!residual || r_dt == WKV7_BF16);
+    wkv7_status done = WKV7_OK;
+#define WKV7_NORM(V, M, R) \
+    done = norm_launch(rmsnorm_fwd_kernel<V, M, R>, P, grid, threads, V && M <= 2 ? ring_bytes<M, R>(2, threads) : 0, stream)
+    if (vec && narrow) WKV7_NORM_MB(true, false);
+    else if (vec) WKV7_NORM_MB(true, true);
+    else WKV7_NORM_MB(false, true);
 #undef WKV7_NORM
-    return launch_status();
+    return done;
 }
 
 size_t wkv7_rmsnorm_backward_workspace_size(long long rows, int D) {
     using namespace wkv7::mixer;
     if (rows <= 0 || D <= 0 || norm_dims(rows, D) != WKV7_OK) return 0;
-    return (size_t)norm_bwd_grid(rows, D) * D * sizeof(float);
+    return (size_t)norm_grid(rows, D, kNormThreads) * D * sizeof(float);
 }
 
 wkv7_status wkv7_rmsnorm_backward(long long rows, int D, wkv7_dtype s_dt, wkv7_dtype dy_dt, wkv7_dtype g_dt,
@@ -316,23 +495,26 @@ wkv7_status wkv7_rmsnorm_backward(long long rows, int D, wkv7_dtype s_dt, wkv7_d
         (dresidual && !elem_ok(dresidual, g_dt)))
         return WKV7_ERR_INVALID_ARG;
     if ((s_dt == WKV7_E4M3) != (s_scales != nullptr) || !f32_opt(s_scales)) return WKV7_ERR_INVALID_ARG;
-    const long long grid = norm_bwd_grid(rows, D);
+    const long long grid = norm_grid(rows, D, kNormThreads);
     if (grid <= 0) return WKV7_ERR_CUDA;
     if (workspace == nullptr || !aligned_to(workspace, 16) || workspace_bytes < (size_t)grid * D * sizeof(float))
         return WKV7_ERR_INVALID_ARG;
-    const NormBwd P{rows, D, s_dt, dy_dt, g_dt, s, s_scales, rstd, weight, dy, dresidual, dx, (float *)workspace};
+    const NormBwd P{rows, D, s_dt, dy_dt, g_dt, s, s_scales, rstd, weight, dy, dresidual, dx, (float *)workspace,
+                    (float)(1.0 / D)};
     const bool vec = D % 4 == 0 && aligned_to(s, 4 * dtype_size(s_dt)) && aligned_to(dy, 4 * dtype_size(dy_dt)) &&
                      aligned_to(dresidual, 4 * dtype_size(g_dt)) && aligned_to(dx, 4 * dtype_size(g_dt)) &&
                      aligned_to(weight, 16);
-    const int nblk = blocks_of(D), mb = norm_batch(nblk), threads = 32 * ((nblk + mb - 1) / mb);
-#define WKV7_NORM(V, M) rmsnorm_bwd_kernel<V, M><<<(unsigned)grid, threads, 0, stream>>>(P)
-#define WKV7_NORM_MB(V)                                                                                   \
-    (mb == 1 ? (void)(WKV7_NORM(V, 1)) : mb == 2 ? (void)(WKV7_NORM(V, 2)) : mb == 4 ? (void)(WKV7_NORM(V, 4)) \
-                                                                            : (void)(WKV7_NORM(V, 8)))
-    if (vec) WKV7_NORM_MB(true);
-    else WKV7_NORM_MB(false);
-#undef WKV7_NORM_MB
+    const int mb = norm_batch(blocks_of(D)), threads = norm_threads(blocks_of(D));
+    const bool narrow = s_dt != WKV7_F32 && dy_dt == WKV7_BF16 && (!dresidual || g_dt == WKV7_BF16);
+    wkv7_status done = WKV7_OK;
+#define WKV7_NORM(V, M, R)                                                                                      \
+    done = norm_launch(rmsnorm_bwd_kernel<V, M, R>, P, grid, threads,                                           \
+                       M > 2 ? (size_t)4 * M * threads * sizeof(float) : V ? ring_bytes<M, R>(3, threads) : 0, stream)
+    if (vec && narrow) WKV7_NORM_MB(true, false);
+    else if (vec) WKV7_NORM_MB(true, true);
+    else WKV7_NORM_MB(false, true);
 #undef WKV7_NORM
+    if (done != WKV7_OK) return done;
     sum_parts(grid, D, (const float *)workspace, dweight, stream);
     return launch_status();
 }

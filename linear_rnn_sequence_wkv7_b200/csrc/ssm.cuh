@@ -10,17 +10,18 @@ namespace wkv7 {
 namespace mixer {
 
 constexpr int kTile = 16;           // tokens a tile, and between saved states
-constexpr int kScanThreads = 128;
 
-// lanes that share a channel pair: 4 n each
-inline int scan_lanes(int N) { return N <= 8 ? 2 : N <= 16 ? 4 : N <= 32 ? 8 : 16; }
-__host__ __device__ constexpr int scan_channels(int LN) { return 2 * kScanThreads / LN; }
+// N padded to 8, 16, 32 or 64.  A thread holds NPT (4 or 2) of a channel's n; the
+// NP / NPT lanes of a channel sit side by side.
+inline int scan_pad(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
+__host__ __device__ constexpr int scan_channels(int NP) { return NP == 8 ? 32 : 16; }      // of a block
+__host__ __device__ constexpr int scan_threads(int NP, int NPT) { return scan_channels(NP) * NP / NPT; }
 
-template <typename F> void by_lanes(int LN, F &&f) {
-    if (LN == 2) f(std::integral_constant<int, 2>{});
-    else if (LN == 4) f(std::integral_constant<int, 4>{});
-    else if (LN == 8) f(std::integral_constant<int, 8>{});
-    else f(std::integral_constant<int, 16>{});
+template <typename F> void by_pad(int NP, F &&f) {
+    if (NP == 8) f(std::integral_constant<int, 8>{});
+    else if (NP == 16) f(std::integral_constant<int, 16>{});
+    else if (NP == 32) f(std::integral_constant<int, 32>{});
+    else f(std::integral_constant<int, 64>{});
 }
 
 struct ScanArgs {
@@ -42,41 +43,138 @@ struct ScanArgs {
 
 __device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
 
-// four numbers of a channel's state row; N need not be a multiple of 4
-__device__ __forceinline__ void store_state(float *to, int N, int ns, const float2 (&h)[2]) {
-    if ((N & 3) == 0) {
-        if (ns < N) *reinterpret_cast<float4 *>(to) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-    } else {
-        const float v[4] = {h[0].x, h[0].y, h[1].x, h[1].y};
+// Four n of a token's B or C; `left`: how many are there
+template <typename T, bool VEC> struct Quad {
+    Vec<T, VEC ? 4 : 1> v[VEC ? 1 : 4];
+    __device__ __forceinline__ void load(const T *p, int left) {
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-            if (ns + n < N) to[n] = v[n];
+        for (int i = 0; i < (VEC ? 1 : 4); ++i) {
+            v[i].zero();
+            if (i < left) v[i].load(p + i);
+        }
+    }
+    // to shared memory, in the order 0 xor p, 1 xor p, ...
+    __device__ __forceinline__ void put(float *to, int p = 0) const {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = VEC ? v[0].w[VEC ? i % (sizeof(v[0].w) / 4) : 0] : v[VEC ? 0 : i].w[0];
+        *reinterpret_cast<uint4 *>(to) = make_uint4(w[0 ^ p], w[1 ^ p], w[2 ^ p], w[3 ^ p]);
+    }
+    __device__ __forceinline__ void put(bf16 *to, int p = 0) const {
+        uint32_t w[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = VEC ? v[0].w[VEC ? i : 0] : (v[VEC ? 0 : 2 * i].w[0] | (v[VEC ? 0 : 2 * i + 1].w[0] << 16));
+        if (p & 1) w[0] = __byte_perm(w[0], 0, 0x1032), w[1] = __byte_perm(w[1], 0, 0x1032);
+        *reinterpret_cast<uint2 *>(to) = (p & 2) ? make_uint2(w[1], w[0]) : make_uint2(w[0], w[1]);
+    }
+};
+
+// A thread's numbers of a channel's state row, n = ns .. ns + NPT - 1; N need not be a multiple of NPT
+template <int NPT> __device__ __forceinline__ void store_state(float *row, int N, int ns, const float2 (&h)[NPT / 2]) {
+    if (N % NPT == 0) {
+        if (ns >= N) return;
+        if constexpr (NPT == 4) *reinterpret_cast<float4 *>(row + ns) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
+        else *reinterpret_cast<float2 *>(row + ns) = h[0];
+    } else {
+#pragma unroll
+        for (int n = 0; n < NPT; ++n)
+            if (ns + n < N) row[ns + n] = (n & 1) ? h[n / 2].y : h[n / 2].x;
+    }
+}
+template <int NPT> __device__ __forceinline__ void load_state(const float *row, int N, int ns, float2 (&h)[NPT / 2]) {
+    if (N % NPT == 0) {
+#pragma unroll
+        for (int j = 0; j < NPT / 2; ++j) h[j] = make_float2(0.f, 0.f);
+        if (ns >= N) return;
+        if constexpr (NPT == 4) {
+            const float4 v = *reinterpret_cast<const float4 *>(row + ns);
+            h[0] = make_float2(v.x, v.y), h[1] = make_float2(v.z, v.w);
+        } else {
+            h[0] = *reinterpret_cast<const float2 *>(row + ns);
+        }
+    } else {
+        float v[NPT];
+#pragma unroll
+        for (int n = 0; n < NPT; ++n) v[n] = ns + n < N ? row[ns + n] : 0.f;
+#pragma unroll
+        for (int j = 0; j < NPT / 2; ++j) h[j] = make_float2(v[2 * j], v[2 * j + 1]);
+    }
+}
+// The rates of a thread's n in units of log 2 (0 for the padding, which keeps a zero state at zero)
+template <int NPT> __device__ __forceinline__ void load_rates(const float *row, int N, int ns, bool live, float2 (&a)[NPT / 2]) {
+#pragma unroll
+    for (int j = 0; j < NPT / 2; ++j) {
+        const int n = ns + 2 * j;
+        a[j].x = (live && n < N) ? __ldg(row + n) * kLog2e : 0.f;
+        a[j].y = (live && n + 1 < N) ? __ldg(row + n + 1) * kLog2e : 0.f;
+    }
+}
+// B and C in shared memory keep their own type: a warp-wide load costs a cycle of
+// the SM's shared memory for every 4 bytes a lane, broadcast or not, and at 16
+// bytes each for B and C that would be the scan's bound.
+// A thread's n of a token:
+template <int NPT> __device__ __forceinline__ void shared_n(const float *p, float2 (&v)[NPT / 2]) {
+    if constexpr (NPT == 4) {
+        const float4 q = *reinterpret_cast<const float4 *>(p);
+        v[0] = make_float2(q.x, q.y), v[1] = make_float2(q.z, q.w);
+    } else {
+        v[0] = *reinterpret_cast<const float2 *>(p);
+    }
+}
+__device__ __forceinline__ float2 bf16_pair(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <int NPT> __device__ __forceinline__ void shared_n(const bf16 *p, float2 (&v)[NPT / 2]) {
+    if constexpr (NPT == 4) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+        v[0] = bf16_pair(q.x), v[1] = bf16_pair(q.y);
+    } else {
+        v[0] = bf16_pair(*reinterpret_cast<const uint32_t *>(p));
     }
 }
 
-// Sums of M values over L lanes side by side (l = lane in the group), scattered:
-// while values are left to share out, a lane keeps the half that its lowest
-// unused bit names and hands the other half over; then plain sums.  Afterwards a
-// lane holds max(M / L, 1) sums, v[i] = that of value i min(L, M) + l mod min(L, M).
-// STRIDE: lanes between neighbours of the group.
-template <int L, int M, int STRIDE = 1> __device__ __forceinline__ void reduce_scatter(float (&v)[M], int l) {
-    int left = M;
+// (a_i, b_i) of V channels in a row
+template <int V> __device__ __forceinline__ void put_pairs(float2 *to, const float (&a)[V], const float (&b)[V]) {
+    if constexpr (V == 1) to[0] = make_float2(a[0], b[0]);
+    else {
 #pragma unroll
-    for (int o = 1; o < L; o <<= 1) {
-        if (left > 1) {
-            left >>= 1;
-            const bool up = l & o;
-#pragma unroll
-            for (int i = 0; i < M / 2; ++i) {
-                if (i >= left) break;
-                const float keep = up ? v[2 * i + 1] : v[2 * i], give = up ? v[2 * i] : v[2 * i + 1];
-                v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o * STRIDE);
-            }
-        } else {
-            v[0] += __shfl_xor_sync(0xffffffffu, v[0], o * STRIDE);
-        }
+        for (int i = 0; i < V; i += 2)
+            *reinterpret_cast<float4 *>(to + i) = make_float4(a[i], b[i], a[i + 1], b[i + 1]);
     }
 }
+
+// Sums over the LN lanes of a channel, through shared memory: [kTile][LN][CC]
+// partial values, the planes and rows shifted so that neither the lanes' stores
+// nor the loads of four channels in a row meet in a bank.
+template <int CC, int LN> struct Planes {
+    static constexpr int PS = CC + 32 / LN, RS = LN * PS + (CC == 16 ? 16 : 0), FLOATS = kTile * RS;
+    static __device__ __forceinline__ void put(float *s, int k, int ch, int nl, float v) { s[k * RS + nl * PS + ch] = v; }
+    template <int V> static __device__ __forceinline__ void sum(const float *s, int k, int ch, float (&out)[V]) {
+        const float *p = s + k * RS + ch;
+        if constexpr (V % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < V; i += 4) {
+                float4 t = *reinterpret_cast<const float4 *>(p + i);
+                float2 x = make_float2(t.x, t.y), y = make_float2(t.z, t.w);
+#pragma unroll
+                for (int l = 1; l < LN; ++l) {
+                    t = *reinterpret_cast<const float4 *>(p + l * PS + i);
+                    x = __fadd2_rn(x, make_float2(t.x, t.y)), y = __fadd2_rn(y, make_float2(t.z, t.w));
+                }
+                out[i] = x.x, out[i + 1] = x.y, out[i + 2] = y.x, out[i + 3] = y.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                float t = p[i];
+#pragma unroll
+                for (int l = 1; l < LN; ++l) t += p[l * PS + i];
+                out[i] = t;
+            }
+        }
+    }
+};
 
 }  // namespace mixer
 }  // namespace wkv7

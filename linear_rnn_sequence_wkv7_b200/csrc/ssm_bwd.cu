@@ -7,18 +7,23 @@
 //     d(dt)_t = u_t sum_n g_t B_t + sum_n A p_t g_t,   ddelta = d(dt) softplus'
 //     dA = sum_t dt_t p_t g_t       dD = sum ds u       dz = dy s (z sigmoid(z))'
 //
-// Layout as in the forward (2 channels x 4 n a thread, tiles of 16 tokens).  A
-// block walks its tiles from the last to the first.  For each it starts from the
-// state saved before the tile, replays the 16 tokens with every h in registers
-// (128 of them, both loops unrolled), then runs the adjoint back over them.
-// Bound: two exponentials per (token, channel, n), one a replay and one a way
-// back, and about 200 multiply-adds a channel-token at N = 16.
+// A thread holds 4 n of one channel, the lanes of a channel side by side, 256
+// threads a block (64 channels at N = 16).  A block walks its tiles of 16 tokens
+// from the last to the first, each in two halves: from the state saved before the
+// tile it replays the half's 8 tokens with every h in registers (32; all 16 tokens
+// at once spilled at the 128 registers that two blocks an SM allow), then runs the
+// adjoint back over them.  Bound: 2.5 exponentials per (token, channel, n), 1.5 in
+// the replays and one on the way back, and about as many cycles of issue: some 80
+// instructions a warp for 8 channels of a token.
 //
-// dB and dC join channels: 8 values over the lanes of a warp that share n,
-// scattered while they are summed (7 exchanges for 8 lanes); the block's warps
-// join in shared memory, the blocks through partial sums added up in order by a
-// second kernel.  Few channels over many tokens: segments, as in the forward
-// (summaries from a zero adjoint, a chain from the last segment to the first).
+// Sums over n (C . h, g . B, A . p g) go to shared memory lane by lane and are
+// added up by the threads that write the outputs.  Sums over channels (dB, dC) run
+// over the lanes of a warp by exchanges: a lane's four n are kept in an order of
+// its own, slot j holding n = j xor (channel group mod 4), so that the half to
+// hand over at a step is the same registers in every lane and needs no selects.
+// The warps join in shared memory, the blocks through partial sums added up in
+// order by a second kernel.  Few channels over many tokens: segments, as in the
+// forward (summaries from a zero adjoint, a chain from the last to the first).
 #include "ssm.cuh"
 
 namespace wkv7 {
@@ -30,7 +35,7 @@ int ssm_segments(int B, int T, int D, int N, int G, int sms);
 size_t ssm_segment_bytes(int B, int D, int N, int nseg);
 void ssm_fwd_all(ScanArgs P, const float *state0, int nseg, char *ws, wkv7_dtype dt, bool vec, bool y,
                  cudaStream_t st);
-bool ssm_vec(const ScanArgs &P, wkv7_dtype dt, const void *more, size_t more_size);
+bool ssm_vec(const ScanArgs &P, wkv7_dtype dt);
 
 namespace {
 
@@ -47,23 +52,25 @@ struct BwdArgs {
     float *seg_g, *seg_dt;          // summaries
 };
 
-template <typename T, int LN, int V>
-__global__ void __launch_bounds__(kScanThreads)
+// A segment's own adjoint (from zero behind it) and sum of dt
+template <typename T, int NP, bool VEC>
+__global__ void __launch_bounds__(scan_threads(NP, 4))
 ssm_bwd_summary_kernel(const BwdArgs K) {
     const ScanArgs &P = K.f;
-    constexpr int CC = scan_channels(LN), NP = 4 * LN;
-    constexpr int EPT = kTile * CC / kScanThreads, Q = EPT / V, NB = kTile * NP / kScanThreads;
+    constexpr int CC = scan_channels(NP), LN = NP / 4, THREADS = CC * LN;
+    constexpr int EPT = kTile * CC / THREADS, V = VEC ? EPT : 1, Q = EPT / V;
+    constexpr int IB = kTile * NP / 4, NB = (IB + THREADS - 1) / THREADS;
     constexpr bool PRECISE = sizeof(T) == 4;
-    __shared__ __align__(16) float s_dt[kTile][CC], s_ds[kTile][CC];
-    __shared__ float4 s_C[kTile][LN];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long id = blockIdx.x;
-    const int tile_c = (int)(id % P.tiles);
-    id /= P.tiles;
-    const int g = (int)(id % P.G);
-    id /= P.G;
-    const long long b = id % P.B;
-    const int seg = (int)(id / P.B);
+    __shared__ __align__(16) float2 s_dd[kTile][CC];        // dt, ds
+    __shared__ __align__(16) T s_C[kTile][NP];
+    const int tid = threadIdx.x;
+    unsigned id = blockIdx.x;
+    const int per_g = (P.Dg + CC - 1) / CC, tile_c = (int)(id % (unsigned)per_g);
+    id /= (unsigned)per_g;
+    const int g = (int)(id % (unsigned)P.G);
+    id /= (unsigned)P.G;
+    const long long b = id % (unsigned)P.B;
+    const int seg = (int)(id / (unsigned)P.B);
     const int c0 = g * P.Dg + tile_c * CC, c1 = (g + 1) * P.Dg;
     const int t0 = (int)min((long long)seg * P.seg_len, (long long)P.T);
     const int t1 = (int)min((long long)t0 + P.seg_len, (long long)P.T);
@@ -73,76 +80,76 @@ ssm_bwd_summary_kernel(const BwdArgs K) {
     const T *z = P.z ? static_cast<const T *>(P.z) + b * P.z_bs + lc : nullptr;
     const T *dy = static_cast<const T *>(K.dy) + (size_t)b * P.T * P.D + lc;
     const T *Cm = static_cast<const T *>(P.Cm) + b * P.c_bs + g * P.N;
-    const int nl = lane % LN, cl = (warp * (32 / LN) + lane / LN) * 2, cs = c0 + cl, ns = 4 * nl;
-    float2 a2[2][2], w[2][2];
+    const int nl = tid % LN, cl = tid / LN, cs = c0 + cl, ns = 4 * nl;
+    float2 a2[2], w[2];
+    load_rates<4>(P.A + (size_t)cs * P.N, P.N, ns, cs < c1, a2);
+    w[0] = w[1] = make_float2(0.f, 0.f);
+    float bias[V];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        float av[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-            av[n] = (cs + c < c1 && ns + n < P.N) ? __ldg(P.A + (size_t)(cs + c) * P.N + ns + n) * kLog2e : 0.f;
-        a2[c][0] = make_float2(av[0], av[1]), a2[c][1] = make_float2(av[2], av[3]);
-        w[c][0] = w[c][1] = make_float2(0.f, 0.f);
-    }
-    double sum0 = 0, sum1 = 0;
-    for (int t = t0 + (t1 - 1 - t0) / kTile * kTile; t >= t0 && t1 > t0; t -= kTile) {
-        __syncthreads();
+    for (int i = 0; i < V; ++i) bias[i] = (live && P.dt_bias) ? __ldg(P.dt_bias + lc + i) : 0.f;
+    double sum = 0;
+    Vec<T, V> nd[Q], ng[Q], nz[Q];
+    Quad<T, VEC> nc[NB];
+    auto fetch = [&](int t) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            const int k = lt + q * (kTile / Q), tt = t + k;
-            float fd[V], fg[V];
-#pragma unroll
-            for (int i = 0; i < V; ++i) fd[i] = fg[i] = 0.f;
+            const int tt = t + lt + q * (kTile / Q);
+            nd[q].zero(), ng[q].zero(), nz[q].zero();
             if (live && tt < t1) {
-                Vec<T, V> d, e, v;
-                d.load(de + tt * P.d_ts);
-                e.load(dy + (size_t)tt * P.D);
-                v.zero();
-                if (z) v.load(z + tt * P.z_ts);
-                float fz[V];
-                d.get(fd), e.get(fg), v.get(fz);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float x = fd[i] + (P.dt_bias ? __ldg(P.dt_bias + lc + i) : 0.f);
-                    fd[i] = P.softplus ? softplus(x) : x;
-                    if (z) fg[i] *= fz[i] * sigmoid<PRECISE>(fz[i]);
-                }
+                nd[q].load(de + tt * P.d_ts);
+                ng[q].load(dy + (size_t)tt * P.D);
+                if (z) nz[q].load(z + tt * P.z_ts);
             }
-            storev<V>(&s_dt[k][lc - c0], fd);
-            storev<V>(&s_ds[k][lc - c0], fg);
         }
 #pragma unroll
         for (int q = 0; q < NB; ++q) {
-            const int e = tid + q * kScanThreads, tt = t + e / NP, n = e % NP;
-            reinterpret_cast<float *>(s_C)[e] = (tt < t1 && n < P.N) ? to_f32(Cm[tt * P.c_ts + n]) : 0.f;
+            const int e = tid + q * THREADS, tt = t + e / (NP / 4), n = e % (NP / 4) * 4;
+            nc[q].load(Cm + tt * P.c_ts + n, e < IB && tt < t1 ? P.N - n : 0);
+        }
+    };
+    const int last = t0 + (t1 - 1 - t0) / kTile * kTile;
+    if (t0 < t1) fetch(last);
+    for (int t = last; t >= t0 && t1 > t0; t -= kTile) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) {
+            const int k = lt + q * (kTile / Q);
+            const bool in = live && t + k < t1;
+            float fd[V], fg[V], fz[V];
+            nd[q].get(fd), ng[q].get(fg), nz[q].get(fz);
+#pragma unroll
+            for (int i = 0; i < V; ++i) fd[i] += bias[i];
+            if (P.softplus) softplus_all<PRECISE>(fd);
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                if (z) fg[i] *= fz[i] * sigmoid<PRECISE>(fz[i]);
+                fd[i] = in ? fd[i] : 0.f, fg[i] = in ? fg[i] : 0.f;
+            }
+            put_pairs<V>(&s_dd[k][lc - c0], fd, fg);
+        }
+#pragma unroll
+        for (int q = 0; q < NB; ++q) {
+            const int e = tid + q * THREADS;
+            if (e < IB) nc[q].put(&s_C[0][0] + 4 * e);
         }
         __syncthreads();
-        float part0 = 0.f, part1 = 0.f;
-#pragma unroll 2
+        if (t - kTile >= t0) fetch(t - kTile);
+        float part = 0.f;
+#pragma unroll
         for (int k = kTile - 1; k >= 0; --k) {
-            const float2 dt = *reinterpret_cast<const float2 *>(&s_dt[k][cl]);
-            const float2 ds = *reinterpret_cast<const float2 *>(&s_ds[k][cl]);
-            const float4 C = s_C[k][nl];
-            const float2 C2[2] = {make_float2(C.x, C.y), make_float2(C.z, C.w)};
+            const float2 dd = s_dd[k][cl], d2 = make_float2(dd.x, dd.x), e2 = make_float2(dd.y, dd.y);
+            float2 C[2];
+            shared_n<4>(&s_C[k][ns], C);
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float d = c ? dt.y : dt.x, e = c ? ds.y : ds.x;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    w[c][j] = __fmul2_rn(ex2(__fmul2_rn(make_float2(d, d), a2[c][j])),
-                                         __ffma2_rn(make_float2(e, e), C2[j], w[c][j]));
-            }
-            part0 += dt.x, part1 += dt.y;
+            for (int j = 0; j < 2; ++j) w[j] = __fmul2_rn(ex2(__fmul2_rn(d2, a2[j])), __ffma2_rn(e2, C[j], w[j]));
+            part += dd.x;
         }
-        sum0 += part0, sum1 += part1;
+        sum += part;
+        __syncthreads();
     }
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        if (cs + c >= c1) continue;
-        const size_t at = ((size_t)seg * P.B + b) * P.D + cs + c;
-        store_state(K.seg_g + at * P.N + ns, P.N, ns, w[c]);
-        if (nl == 0) K.seg_dt[at] = (float)(c ? sum1 : sum0);
-    }
+    if (cs >= c1) return;
+    const size_t at = ((size_t)seg * P.B + b) * P.D + cs;
+    store_state<4>(K.seg_g + at * P.N, P.N, ns, w);
+    if (nl == 0) K.seg_dt[at] = (float)sum;
 }
 
 // Adjoints behind the segments, in place of their own parts, last to first.
@@ -162,35 +169,59 @@ ssm_bwd_chain_kernel(long long total, int N, int nseg, const float *__restrict__
     }
 }
 
-template <typename T, int LN, int V>
-__global__ void __launch_bounds__(kScanThreads, 2)
+constexpr int kBwdThreads = 256;
+__host__ __device__ constexpr int bwd_channels(int NP) { return kBwdThreads * 4 / NP; }      // of a block
+
+// slots <-> n: slot j holds n = j xor p, p = 0 .. 3; its own inverse
+__device__ __forceinline__ void permute(float2 (&v)[2], int p) {
+    const float2 a = v[0], b = v[1];
+    const float2 x = (p & 2) ? b : a, y = (p & 2) ? a : b;
+    v[0] = (p & 1) ? make_float2(x.y, x.x) : x;
+    v[1] = (p & 1) ? make_float2(y.y, y.x) : y;
+}
+
+// Shared memory of a block, in floats
+template <typename T, int NP> struct BwdShared {
+    static constexpr int CC = bwd_channels(NP), LN = NP / 4, WARPS = kBwdThreads / 32;
+    using Sum = Planes<CC, LN>;
+    static constexpr int DD = 0;                                // [kTile][CC] dt, dt u
+    static constexpr int DS = DD + 2 * kTile * CC;              // [kTile][CC]
+    static constexpr int BC = DS + kTile * CC;                  // T [2][kTile][4][NP]: each token's n in four orders
+    static constexpr int Y = BC + 2 * kTile * 4 * NP * (int)sizeof(T) / 4;      // C . h, lane by lane
+    static constexpr int GB = Y + Sum::FLOATS;                  // g . B
+    static constexpr int AP = GB + Sum::FLOATS;                 // A . p g
+    static constexpr int PART = AP + Sum::FLOATS;               // [WARPS][kTile][2][NP] dB, dC
+    static constexpr int DA = PART + WARPS * kTile * 2 * NP;    // [8][threads]: sums and their errors
+    static constexpr int ACC = DA + 8 * kBwdThreads;            // [2 V][threads]: dD, ddt_bias
+    static constexpr int FLOATS = ACC + 2 * (kTile / LN) * kBwdThreads;
+};
+
+template <typename T, int NP, bool VEC>
+__global__ void __launch_bounds__(kBwdThreads, NP <= 32 ? 2 : 1)
 ssm_bwd_kernel(const BwdArgs K) {
     const ScanArgs &P = K.f;
-    constexpr int CC = scan_channels(LN), NP = 4 * LN, CG = 32 / LN;    // CG channel pairs a warp
-    constexpr int EPT = kTile * CC / kScanThreads, Q = EPT / V, NB = kTile * NP / kScanThreads;
-    constexpr int WARPS = kScanThreads / 32;
+    using S = BwdShared<T, NP>;
+    using Sum = typename S::Sum;
+    constexpr int CC = S::CC, LN = S::LN, CG = 32 / LN, THREADS = kBwdThreads;      // CG channels a warp
+    constexpr int EPT = kTile / LN, V = VEC ? EPT : 1, Q = EPT / V;
+    constexpr int IB = 2 * kTile * NP / 4, NB = (IB + THREADS - 1) / THREADS;
     constexpr bool PRECISE = sizeof(T) == 4;
     extern __shared__ __align__(16) float smem[];
-    float(*s_dt)[CC] = reinterpret_cast<float(*)[CC]>(smem);            // each [kTile][CC]
-    float(*s_du)[CC] = s_dt + kTile;                                    // dt u
-    float(*s_ds)[CC] = s_du + kTile;
-    float(*s_gb)[CC] = s_ds + kTile;                                    // sum_n g B
-    float(*s_ap)[CC] = s_gb + kTile;                                    // sum_n A p g
-    float(*s_y)[CC] = s_ap + kTile;                                     // C . h
-    float4(*s_B)[LN] = reinterpret_cast<float4(*)[LN]>(s_y + kTile);    // [kTile][LN]
-    float4(*s_C)[LN] = s_B + kTile;
-    float(*s_part)[kTile][2][NP] = reinterpret_cast<float(*)[kTile][2][NP]>(s_C + kTile);   // [WARPS]
-    float *s_acc = reinterpret_cast<float *>(s_part + WARPS);           // [2 V][threads]: dD, ddt_bias
-    float *s_dA = s_acc + 2 * V * kScanThreads;                         // [16][threads]: sums and their errors
+    float2(*s_dd)[CC] = reinterpret_cast<float2(*)[CC]>(smem + S::DD);
+    float(*s_ds)[CC] = reinterpret_cast<float(*)[CC]>(smem + S::DS);
+    T(*s_BC)[kTile][4][NP] = reinterpret_cast<T(*)[kTile][4][NP]>(smem + S::BC);
+    float *s_y = smem + S::Y, *s_gb = smem + S::GB, *s_ap = smem + S::AP;
+    float(*s_part)[kTile][2][NP] = reinterpret_cast<float(*)[kTile][2][NP]>(smem + S::PART);
+    float *s_dA = smem + S::DA, *s_acc = smem + S::ACC;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long id = blockIdx.x;
-    const int tile_c = (int)(id % P.tiles);
-    id /= P.tiles;
-    const int g = (int)(id % P.G);
-    id /= P.G;
-    const long long b = id % P.B;
-    const int seg = (int)(id / P.B);
+    unsigned id = blockIdx.x;
+    const int tile_c = (int)(id % (unsigned)P.tiles);
+    id /= (unsigned)P.tiles;
+    const int g = (int)(id % (unsigned)P.G);
+    id /= (unsigned)P.G;
+    const long long b = id % (unsigned)P.B;
+    const int seg = (int)(id / (unsigned)P.B);
     const int c0 = g * P.Dg + tile_c * CC, c1 = (g + 1) * P.Dg;
     const int t0 = (int)min((long long)seg * P.seg_len, (long long)P.T);
     const int t1 = (int)min((long long)t0 + P.seg_len, (long long)P.T);
@@ -202,187 +233,168 @@ ssm_bwd_kernel(const BwdArgs K) {
     const T *dy = static_cast<const T *>(K.dy) + (size_t)b * P.T * P.D + lc;
     const T *Bm = static_cast<const T *>(P.Bm) + b * P.b_bs + g * P.N;
     const T *Cm = static_cast<const T *>(P.Cm) + b * P.c_bs + g * P.N;
-
-    const int nl = lane % LN, cg = lane / LN, cl = (warp * CG + cg) * 2, cs = c0 + cl, ns = 4 * nl;
-    float2 a2[2][2], w[2][2];       // rates (log2), adjoint carried to the token before
+    float bias[V], skip[V];
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        float av[4], wv[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const bool in = cs + c < c1 && ns + n < P.N;
-            av[n] = in ? __ldg(P.A + (size_t)(cs + c) * P.N + ns + n) * kLog2e : 0.f;
-            wv[n] = (in && K.exit) ? K.exit[(((size_t)seg * P.B + b) * P.D + cs + c) * P.N + ns + n] : 0.f;
-        }
-        a2[c][0] = make_float2(av[0], av[1]), a2[c][1] = make_float2(av[2], av[3]);
-        w[c][0] = make_float2(wv[0], wv[1]), w[c][1] = make_float2(wv[2], wv[3]);
+    for (int i = 0; i < V; ++i) {
+        bias[i] = (live && P.dt_bias) ? __ldg(P.dt_bias + lc + i) : 0.f;
+        skip[i] = (live && P.Dskip) ? __ldg(P.Dskip + lc + i) : 0.f;
     }
-    for (int i = 0; i < 2 * V; ++i) s_acc[i * kScanThreads + tid] = 0.f;
-    for (int i = 0; i < 16; ++i) s_dA[i * kScanThreads + tid] = 0.f;
 
-    for (int t = t0 + (t1 - 1 - t0) / kTile * kTile; t >= t0 && t1 > t0; t -= kTile) {
-        // ---- the tile's inputs
-        Vec<T, V> ru[Q], rd[Q], rz[Q], rg[Q];
+    const int nl = tid % LN, cl = tid / LN, cs = c0 + cl, ns = 4 * nl, cg = lane / LN, order = cg & 3;
+    const bool mine = cs < c1;
+    float2 a2[2], w[2];             // rates (log2), adjoint carried to the token before; by slots
+    load_rates<4>(P.A + (size_t)cs * P.N, P.N, ns, mine, a2);
+    permute(a2, order);
+    w[0] = w[1] = make_float2(0.f, 0.f);
+    if (mine && K.exit) load_state<4>(K.exit + (((size_t)seg * P.B + b) * P.D + cs) * P.N, P.N, ns, w);
+    permute(w, order);
+    for (int i = 0; i < 2 * V; ++i) s_acc[i * THREADS + tid] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s_dA[i * THREADS + tid] = 0.f;
+
+    Vec<T, V> nu[Q], nd[Q], nz[Q], ng[Q], cu[Q], cd[Q], cz[Q], cy[Q];
+    Quad<T, VEC> nb[NB];
+    float2 h0[2];
+    auto fetch = [&](int t) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int tt = t + lt + q * (kTile / Q);
-            ru[q].zero(), rd[q].zero(), rz[q].zero(), rg[q].zero();
+            nu[q].zero(), nd[q].zero(), nz[q].zero(), ng[q].zero();
             if (live && tt < t1) {
-                ru[q].load(u + tt * P.u_ts);
-                rd[q].load(de + tt * P.d_ts);
-                rg[q].load(dy + (size_t)tt * P.D);
-                if (z) rz[q].load(z + tt * P.z_ts);
+                nu[q].load(u + tt * P.u_ts);
+                nd[q].load(de + tt * P.d_ts);
+                ng[q].load(dy + (size_t)tt * P.D);
+                if (z) nz[q].load(z + tt * P.z_ts);
             }
-        }
-        float2 h0[2][2];
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            float hv[4] = {0.f, 0.f, 0.f, 0.f};
-            const float *from = P.states + ((size_t)(b * P.nck + t / kTile) * P.D + cs + c) * P.N + ns;
-            if (cs + c < c1) {
-                if ((P.N & 3) == 0) {
-                    if (ns < P.N) {
-                        const float4 v = __ldg(reinterpret_cast<const float4 *>(from));
-                        hv[0] = v.x, hv[1] = v.y, hv[2] = v.z, hv[3] = v.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int n = 0; n < 4; ++n)
-                        if (ns + n < P.N) hv[n] = __ldg(from + n);
-                }
-            }
-            h0[c][0] = make_float2(hv[0], hv[1]), h0[c][1] = make_float2(hv[2], hv[3]);
         }
 #pragma unroll
         for (int q = 0; q < NB; ++q) {
-            const int e = tid + q * kScanThreads, tt = t + e / NP, n = e % NP;
-            const bool in = tt < t1 && n < P.N;
-            reinterpret_cast<float *>(s_B)[e] = in ? to_f32(Bm[tt * P.b_ts + n]) : 0.f;
-            reinterpret_cast<float *>(s_C)[e] = in ? to_f32(Cm[tt * P.c_ts + n]) : 0.f;
+            const int e = tid + q * THREADS, tt = t + (e / (NP / 4)) % kTile, n = e % (NP / 4) * 4;
+            nb[q].load((e >= IB / 2 ? Cm + tt * P.c_ts : Bm + tt * P.b_ts) + n, e < IB && tt < t1 ? P.N - n : 0);
         }
+    };
+    auto prepare = [&](int t) {     // tokens behind t1: dt = dt u = ds = B = C = 0 change nothing
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int k = lt + q * (kTile / Q), ch = lc - c0;
             const bool in = live && t + k < t1;
             float fu[V], fd[V], fz[V], fg[V];
-            ru[q].get(fu), rd[q].get(fd), rz[q].get(fz), rg[q].get(fg);
+            nu[q].get(fu), nd[q].get(fd), nz[q].get(fz), ng[q].get(fg);
+#pragma unroll
+            for (int i = 0; i < V; ++i) fd[i] += bias[i];
+            if (P.softplus) softplus_all<PRECISE>(fd);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float x = fd[i] + ((in && P.dt_bias) ? __ldg(P.dt_bias + lc + i) : 0.f);
-                fd[i] = in ? (P.softplus ? softplus(x) : x) : 0.f;
-                fu[i] = fd[i] != 0.f ? fd[i] * fu[i] : 0.f;
                 if (z) fg[i] *= fz[i] * sigmoid<PRECISE>(fz[i]);
+                fd[i] = in ? fd[i] : 0.f, fu[i] = in ? fd[i] * fu[i] : 0.f, fg[i] = in ? fg[i] : 0.f;
             }
-            storev<V>(&s_dt[k][ch], fd);
-            storev<V>(&s_du[k][ch], fu);
+            put_pairs<V>(&s_dd[k][ch], fd, fu);
             storev<V>(&s_ds[k][ch], fg);
+            cu[q] = nu[q], cd[q] = nd[q], cz[q] = nz[q], cy[q] = ng[q];
         }
-        __syncthreads();
+#pragma unroll
+        for (int q = 0; q < NB; ++q) {
+            const int e = tid + q * THREADS;
+            if (e >= IB) continue;
+            T *to = &s_BC[e / (IB / 2)][(e / (NP / 4)) % kTile][0][e % (NP / 4) * 4];
+#pragma unroll
+            for (int p = 0; p < 4; ++p) nb[q].put(to + p * NP, p);
+        }
+        h0[0] = h0[1] = make_float2(0.f, 0.f);
+        if (mine) load_state<4>(P.states + ((size_t)(b * P.nck + t / kTile) * P.D + cs) * P.N, P.N, ns, h0);
+        permute(h0, order);
+    };
 
-        // ---- replay: every h of the tile
-        float2 h[kTile][2][2];
+    const int last = t0 + (t1 - 1 - t0) / kTile * kTile;
+    if (t0 < t1) {
+        fetch(last);
+        prepare(last);
+        __syncthreads();
+    }
+    for (int t = last; t >= t0 && t1 > t0; t -= kTile) {
+        if (t - kTile >= t0) fetch(t - kTile);
+
+        float2 dA[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+        for (int half = kTile / 2; half >= 0; half -= kTile / 2) {
+        // ---- replay: the state up to the half, then every h of it
+        float2 h[kTile / 2][2], hs[2] = {h0[0], h0[1]};
+        auto advance = [&](int k, const float2 (&from)[2], float2 (&to)[2]) {
+            const float2 dd = s_dd[k][cl], d2 = make_float2(dd.x, dd.x), v2 = make_float2(dd.y, dd.y);
+            float2 B[2];
+            shared_n<4>(&s_BC[0][k][order][ns], B);
 #pragma unroll
-        for (int k = 0; k < kTile; ++k) {
-            const float2 dt = *reinterpret_cast<const float2 *>(&s_dt[k][cl]);
-            const float2 du = *reinterpret_cast<const float2 *>(&s_du[k][cl]);
-            const float4 B = s_B[k][nl];
-            const float2 B2[2] = {make_float2(B.x, B.y), make_float2(B.z, B.w)};
+            for (int j = 0; j < 2; ++j) to[j] = __ffma2_rn(ex2(__fmul2_rn(d2, a2[j])), from[j], __fmul2_rn(v2, B[j]));
+        };
+        if (half) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float d = c ? dt.y : dt.x, v = c ? du.y : du.x;
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    h[k][c][j] = __ffma2_rn(ex2(__fmul2_rn(make_float2(d, d), a2[c][j])), k ? h[k - 1][c][j] : h0[c][j],
-                                            __fmul2_rn(make_float2(v, v), B2[j]));
-            }
+            for (int k = 0; k < kTile / 2; ++k) advance(k, hs, hs);
         }
-        if (z) {
 #pragma unroll
-            for (int k = 0; k < kTile; k += 2) {
-                float yv[4];
-#pragma unroll
-                for (int kk = 0; kk < 2; ++kk) {
-                    const float4 C = s_C[k + kk][nl];
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float2 p = __ffma2_rn(h[k + kk][c][0], make_float2(C.x, C.y),
-                                                    __fmul2_rn(h[k + kk][c][1], make_float2(C.z, C.w)));
-                        yv[2 * kk + c] = p.x + p.y;
-                    }
-                }
-                reduce_scatter<LN, 4>(yv, nl);
-                if constexpr (LN == 2) {
-                    s_y[k][cl + nl] = yv[0];
-                    s_y[k + 1][cl + nl] = yv[1];
-                } else if (nl < 4) {
-                    s_y[k + (nl >> 1)][cl + (nl & 1)] = yv[0];
-                }
-            }
-        }
+        for (int k = 0; k < kTile / 2; ++k) advance(half + k, k ? h[k - 1] : hs, h[k]);
 
         // ---- the way back
-        float2 dA[2][2];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) dA[c][0] = dA[c][1] = make_float2(0.f, 0.f);
-#pragma unroll
-        for (int k = kTile - 1; k >= 0; --k) {
-            const float2 dt = *reinterpret_cast<const float2 *>(&s_dt[k][cl]);
-            const float2 du = *reinterpret_cast<const float2 *>(&s_du[k][cl]);
-            const float2 ds = *reinterpret_cast<const float2 *>(&s_ds[k][cl]);
-            const float4 B = s_B[k][nl], C = s_C[k][nl];
-            const float2 B2[2] = {make_float2(B.x, B.y), make_float2(B.z, B.w)};
-            const float2 C2[2] = {make_float2(C.x, C.y), make_float2(C.z, C.w)};
-            float2 dB2[2], dC2[2];
-            float r[4];                             // sum_n g B and sum_n A p g of both channels
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const float d = c ? dt.y : dt.x, v = c ? du.y : du.x, e = c ? ds.y : ds.x;
-                const float2 d2 = make_float2(d, d), v2 = make_float2(v, v), e2 = make_float2(e, e);
-                float2 gb, ap;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float2 hp = k ? h[k - 1][c][j] : h0[c][j];
-                    const float2 a = ex2(__fmul2_rn(d2, a2[c][j]));
-                    const float2 gg = __ffma2_rn(e2, C2[j], w[c][j]);
-                    const float2 q = __fmul2_rn(__fmul2_rn(a, hp), gg);
-                    dC2[j] = c ? __ffma2_rn(e2, h[k][c][j], dC2[j]) : __fmul2_rn(e2, h[k][c][j]);
-                    dB2[j] = c ? __ffma2_rn(v2, gg, dB2[j]) : __fmul2_rn(v2, gg);
-                    gb = j ? __ffma2_rn(gg, B2[j], gb) : __fmul2_rn(gg, B2[j]);
-                    ap = j ? __ffma2_rn(q, a2[c][j], ap) : __fmul2_rn(q, a2[c][j]);
-                    dA[c][j] = __ffma2_rn(q, d2, dA[c][j]);
-                    w[c][j] = __fmul2_rn(a, gg);
-                }
-                r[c] = gb.x + gb.y;
-                r[2 + c] = ap.x + ap.y;
+        for (int i = kTile / 2 - 1; i >= 0; --i) {
+            const int k = half + i;
+            const float2 dd = s_dd[k][cl], d2 = make_float2(dd.x, dd.x), v2 = make_float2(dd.y, dd.y);
+            const float e = s_ds[k][cl];
+            const float2 e2 = make_float2(e, e);
+            float2 B[2], C[2], gg[2], dB[2], dC[2], q[2];
+            shared_n<4>(&s_BC[0][k][order][ns], B);
+            shared_n<4>(&s_BC[1][k][order][ns], C);
+            if (z) {
+                const float2 y = __ffma2_rn(h[i][1], C[1], __fmul2_rn(h[i][0], C[0]));
+                Sum::put(s_y, k, cl, nl, y.x + y.y);
             }
-            reduce_scatter<LN, 4>(r, nl);
-            if constexpr (LN == 2) {
-                s_gb[k][cl + nl] = r[0];
-                s_ap[k][cl + nl] = r[1];
-            } else if (nl < 4) {
-                ((nl >> 1) ? s_ap : s_gb)[k][cl + (nl & 1)] = r[0];
-            }
-            float bc[8] = {dB2[0].x, dB2[0].y, dB2[1].x, dB2[1].y, dC2[0].x, dC2[0].y, dC2[1].x, dC2[1].y};
-            reduce_scatter<CG, 8, LN>(bc, cg);
-            constexpr int KEEP = CG < 8 ? 8 / CG : 1, LOW = CG < 8 ? CG : 8;
-            if (cg < LOW) {
 #pragma unroll
-                for (int i = 0; i < KEEP; ++i) {
-                    const int v = i * LOW + cg;     // 4 of dB, then 4 of dC
-                    s_part[warp][k][v >> 2][ns + (v & 3)] = bc[i];
-                }
+            for (int j = 0; j < 2; ++j) {
+                const float2 a = ex2(__fmul2_rn(d2, a2[j]));
+                gg[j] = __ffma2_rn(e2, C[j], w[j]);
+                w[j] = __fmul2_rn(a, gg[j]);
+                q[j] = __fmul2_rn(w[j], i ? h[i ? i - 1 : 0][j] : hs[j]);       // p g
+                dA[j] = __ffma2_rn(q[j], d2, dA[j]);
+                dB[j] = __fmul2_rn(v2, gg[j]);
+                dC[j] = __fmul2_rn(e2, h[i][j]);
+            }
+            const float2 gb = __ffma2_rn(gg[1], B[1], __fmul2_rn(gg[0], B[0]));
+            const float2 ap = __ffma2_rn(q[1], a2[1], __fmul2_rn(q[0], a2[0]));
+            Sum::put(s_gb, k, cl, nl, gb.x + gb.y);
+            Sum::put(s_ap, k, cl, nl, ap.x + ap.y);
+            // over the warp's channels: lanes LN apart whose orders differ in one bit
+            float bc[2][4] = {{dB[0].x, dB[0].y, dB[1].x, dB[1].y}, {dC[0].x, dC[0].y, dC[1].x, dC[1].y}};
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                bc[m][0] += __shfl_xor_sync(0xffffffffu, bc[m][1], LN);
+                bc[m][2] += __shfl_xor_sync(0xffffffffu, bc[m][3], LN);
+                if constexpr (CG >= 4) bc[m][0] += __shfl_xor_sync(0xffffffffu, bc[m][2], 2 * LN);
+            }
+            float *to = &s_part[warp][k][0][ns + order];
+            if constexpr (CG >= 8) {            // one of dB and dC a lane
+                const bool up = cg & 4;
+                const float give = up ? bc[0][0] : bc[1][0];
+                float r = (up ? bc[1][0] : bc[0][0]) + __shfl_xor_sync(0xffffffffu, give, 4 * LN);
+                if constexpr (CG == 16) r += __shfl_xor_sync(0xffffffffu, r, 8 * LN);
+                if (CG == 8 || cg < 8) to[up ? NP : 0] = r;
+            } else if constexpr (CG == 4) {
+                to[0] = bc[0][0];
+                to[NP] = bc[1][0];
+            } else {                            // two lanes a group: n = order and order xor 2
+                to[0] = bc[0][0];
+                to[NP] = bc[1][0];
+                float *other = &s_part[warp][k][0][ns + (order ^ 2)];
+                other[0] = bc[0][2];
+                other[NP] = bc[1][2];
             }
         }
+        }
         // the tile's part of dA, into a sum with its rounding error kept (two-sum)
-        {
-            const float tile_dA[8] = {dA[0][0].x, dA[0][0].y, dA[0][1].x, dA[0][1].y,
-                                      dA[1][0].x, dA[1][0].y, dA[1][1].x, dA[1][1].y};
+        const float tile_dA[4] = {dA[0].x, dA[0].y, dA[1].x, dA[1].y};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float s = s_dA[2 * i * kScanThreads + tid], x = tile_dA[i], n = s + x, v = n - s;
-                s_dA[2 * i * kScanThreads + tid] = n;
-                s_dA[(2 * i + 1) * kScanThreads + tid] += (s - (n - v)) + (x - v);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float s = s_dA[2 * i * THREADS + tid], x = tile_dA[i], n = s + x, v = n - s;
+            s_dA[2 * i * THREADS + tid] = n;
+            s_dA[(2 * i + 1) * THREADS + tid] += (s - (n - v)) + (x - v);
         }
         __syncthreads();
 
@@ -392,20 +404,24 @@ ssm_bwd_kernel(const BwdArgs K) {
             const int k = lt + q * (kTile / Q), ch = lc - c0;
             if (!live || t + k >= t1) continue;
             float fu[V], fd[V], fz[V], fg[V], odu[V], odd[V], odz[V];
-            ru[q].get(fu), rd[q].get(fd), rz[q].get(fz), rg[q].get(fg);
+            cu[q].get(fu), cd[q].get(fd), cz[q].get(fz), cy[q].get(fg);
+            float gb[V], ap[V], yc[V];
+            Sum::template sum<V>(s_gb, k, ch, gb);
+            Sum::template sum<V>(s_ap, k, ch, ap);
+            if (z) Sum::template sum<V>(s_y, k, ch, yc);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float gb = s_gb[k][ch + i], ap = s_ap[k][ch + i], ds = s_ds[k][ch + i], dt = s_dt[k][ch + i];
-                const float skip = P.Dskip ? __ldg(P.Dskip + lc + i) : 0.f;
-                odu[i] = fmaf(dt, gb, skip * ds);
-                float dd = fmaf(fu[i], gb, ap * 0.6931471805599453f);       // a2 is in units of log 2
-                if (P.softplus) dd *= sigmoid<true>(fd[i] + (P.dt_bias ? __ldg(P.dt_bias + lc + i) : 0.f));
+                const float ds = s_ds[k][ch + i], dt = s_dd[k][ch + i].x;
+                odu[i] = fmaf(dt, gb[i], skip[i] * ds);
+                float dd = fmaf(fu[i], gb[i], ap[i] * 0.6931471805599453f);     // a2 is in units of log 2
+                if (P.softplus) dd *= sigmoid<PRECISE>(fd[i] + bias[i]);
                 odd[i] = dd;
-                s_acc[i * kScanThreads + tid] += ds * fu[i];
-                s_acc[(V + i) * kScanThreads + tid] += dd;
+                s_acc[i * THREADS + tid] += ds * fu[i];
+                s_acc[(V + i) * THREADS + tid] += dd;
                 if (z) {
                     const float sg = sigmoid<PRECISE>(fz[i]);
-                    odz[i] = fg[i] * fmaf(skip, fu[i], s_y[k][ch + i]) * (sg * fmaf(fz[i], 1.f - sg, 1.f));
+                    odz[i] = fg[i] * fmaf(skip[i], fu[i], yc[i]) *
+                             (sg * fmaf(fz[i], 1.f - sg, 1.f));
                 }
             }
             const size_t at = ((size_t)b * P.T + t + k) * P.D + lc;
@@ -420,38 +436,37 @@ ssm_bwd_kernel(const BwdArgs K) {
             }
         }
         const size_t bt = (size_t)P.B * P.T * P.G * P.N;
-        for (int e = tid; e < kTile * 2 * NP; e += kScanThreads) {
+        for (int e = tid; e < kTile * 2 * NP; e += THREADS) {
             const int which = e / (kTile * NP), k = (e / NP) % kTile, n = e % NP;
             if (t + k >= t1 || n >= P.N) continue;
             float s = s_part[0][k][which][n];
 #pragma unroll
-            for (int i = 1; i < WARPS; ++i) s += s_part[i][k][which][n];
+            for (int i = 1; i < S::WARPS; ++i) s += s_part[i][k][which][n];
             K.dbc[((size_t)tile_c * 2 + which) * bt + (((size_t)b * P.T + t + k) * P.G + g) * P.N + n] = s;
         }
+        if (t - kTile >= t0) prepare(t - kTile);
         __syncthreads();
     }
 
     const size_t part = (size_t)seg * P.B + b;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        if (cs + c >= c1) continue;
-        if (seg == 0 && K.dstate0) store_state(K.dstate0 + ((size_t)b * P.D + cs + c) * P.N + ns, P.N, ns, w[c]);
+    if (mine) {
+        permute(w, order);
+        if (seg == 0 && K.dstate0) store_state<4>(K.dstate0 + ((size_t)b * P.D + cs) * P.N, P.N, ns, w);
         float v[4];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
-            v[n] = s_dA[2 * (4 * c + n) * kScanThreads + tid] + s_dA[(2 * (4 * c + n) + 1) * kScanThreads + tid];
-        const float2 v2[2] = {make_float2(v[0], v[1]), make_float2(v[2], v[3])};
-        store_state(K.dA + (part * P.D + cs + c) * P.N + ns, P.N, ns, v2);
+        for (int i = 0; i < 4; ++i) v[i] = s_dA[2 * i * THREADS + tid] + s_dA[(2 * i + 1) * THREADS + tid];
+        float2 v2[2] = {make_float2(v[0], v[1]), make_float2(v[2], v[3])};
+        permute(v2, order);
+        store_state<4>(K.dA + (part * P.D + cs) * P.N, P.N, ns, v2);
     }
     // dD and ddt_bias: the threads that loaded the same channels, in order
     __syncthreads();
     constexpr int PER = CC / V;
-    for (int e = tid; e < 2 * CC; e += kScanThreads) {
+    for (int e = tid; e < 2 * CC; e += THREADS) {
         const int which = e / CC, ch = e % CC;
         if (c0 + ch >= c1) continue;
         float s = 0.f;
-        for (int i = 0; i < kScanThreads / PER; ++i)
-            s += s_acc[(which * V + ch % V) * kScanThreads + i * PER + ch / V];
+        for (int i = 0; i < THREADS / PER; ++i) s += s_acc[(which * V + ch % V) * THREADS + i * PER + ch / V];
         K.dpar[((size_t)which * P.nseg * P.B + part) * P.D + c0 + ch] = s;
     }
 }
@@ -469,35 +484,35 @@ ssm_dbc_kernel(long long n, int tiles, const float *__restrict__ partial, GT *__
     else dC[i - n] = from_f32<GT>(s);
 }
 
-template <int LN, int V> constexpr size_t bwd_smem() {
-    return sizeof(float) * ((size_t)6 * kTile * scan_channels(LN) + 2 * kTile * 4 * LN +
-                            (size_t)(kScanThreads / 32) * kTile * 2 * 4 * LN + 2 * V * kScanThreads + 16 * kScanThreads);
-}
-
-template <typename T, int LN, int V>
+template <typename T, int NP, bool VEC>
 cudaError_t launch_bwd(const BwdArgs &K, const float *dstateT, cudaStream_t st) {
     const ScanArgs &P = K.f;
-    const unsigned grid = (unsigned)((long long)P.nseg * P.B * P.G * P.tiles);
     BwdArgs M = K;
     M.exit = dstateT;
     if (P.nseg > 1) {
-        ssm_bwd_summary_kernel<T, LN, V><<<grid, kScanThreads, 0, st>>>(K);
+        const long long blocks = (long long)P.nseg * P.B * P.G * ((P.Dg + scan_channels(NP) - 1) / scan_channels(NP));
+        ssm_bwd_summary_kernel<T, NP, VEC><<<(unsigned)blocks, scan_threads(NP, 4), 0, st>>>(K);
         const long long total = (long long)P.B * P.D * P.N;
         ssm_bwd_chain_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(total, P.N, P.nseg, P.A, P.D, dstateT,
                                                                              K.seg_dt, K.seg_g);
         M.exit = K.seg_g;
     }
-    constexpr size_t smem = bwd_smem<LN, V>();
+    constexpr size_t smem = BwdShared<T, NP>::FLOATS * sizeof(float);
     const cudaError_t e =
-        cudaFuncSetAttribute(ssm_bwd_kernel<T, LN, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(ssm_bwd_kernel<T, NP, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    ssm_bwd_kernel<T, LN, V><<<grid, kScanThreads, smem, st>>>(M);
+    ssm_bwd_kernel<T, NP, VEC><<<(unsigned)((long long)P.nseg * P.B * P.G * P.tiles), kBwdThreads, smem, st>>>(M);
     return cudaGetLastError();
 }
 
+int bwd_tiles(int D, int N, int G) {
+    const int CC = bwd_channels(scan_pad(N));
+    return (D / G + CC - 1) / CC;
+}
+// Segments of a backward: two blocks an SM, if that makes at least two segments
+// (whose summaries cost about a third of a pass), each of at least 64 tokens.
 int bwd_segments(int B, int T, int D, int N, int G, int sms) {
-    const int CC = scan_channels(scan_lanes(N)), tiles = (D / G + CC - 1) / CC;
-    const long long blocks = (long long)B * G * tiles;
+    const long long blocks = (long long)B * G * bwd_tiles(D, N, G);
     if (blocks <= 0 || sms <= 0) return 1;
     const long long want = (long long)sms * 2 / blocks, most = T / 64;
     const long long s = want < most ? want : most;
@@ -510,7 +525,7 @@ struct BwdSpace {
 };
 BwdSpace bwd_space(int B, int T, int D, int N, int G, bool with_states) {
     BwdSpace w{};
-    const int sms = sm_count(), CC = scan_channels(scan_lanes(N)), tiles = (D / G + CC - 1) / CC;
+    const int sms = sm_count(), tiles = bwd_tiles(D, N, G);
     w.nseg = bwd_segments(B, T, D, N, G, sms);
     w.fseg = ssm_segments(B, T, D, N, G, sms);
     w.states = with_states ? 0 : round256((size_t)B * ((T + kTile - 1) / kTile) * D * N * 4);
@@ -580,15 +595,15 @@ wkv7_status wkv7_ssm_backward(int B, int T, int D, int N, int G, wkv7_dtype in_d
     BwdArgs K{};
     ScanArgs &P = K.f;
     P.B = B, P.T = T, P.D = D, P.N = N, P.G = G, P.Dg = D / G;
-    P.tiles = (P.Dg + scan_channels(scan_lanes(N)) - 1) / scan_channels(scan_lanes(N));
     P.u = u, P.u_bs = u_bs, P.u_ts = u_ts, P.delta = delta, P.d_bs = d_bs, P.d_ts = d_ts;
     P.z = z, P.z_bs = z_bs, P.z_ts = z_ts;
     P.Bm = Bm, P.b_bs = b_bs, P.b_ts = b_ts, P.Cm = Cm, P.c_bs = c_bs, P.c_ts = c_ts;
     P.A = A, P.Dskip = Dskip, P.dt_bias = dt_bias, P.softplus = softplus;
     P.nck = (T + kTile - 1) / kTile;
-    const bool vec = ssm_vec(P, in_dt, dy, 16) && aligned_to(du, 16) && aligned_to(ddelta, 16) && aligned_to(dz, 16);
+    const bool vec = ssm_vec(P, in_dt) && aligned_to(dy, 16) && aligned_to(du, 16) && aligned_to(ddelta, 16) && aligned_to(dz, 16);
     if (states == nullptr) {
         P.states = (float *)take(w.states);
+        P.tiles = (P.Dg + scan_channels(scan_pad(N)) - 1) / scan_channels(scan_pad(N));
         ssm_fwd_all(P, state0, w.fseg, take(w.fwd), in_dt, vec, false, stream);
     } else {
         P.states = const_cast<float *>(states);         // read only from here on
@@ -598,14 +613,14 @@ wkv7_status wkv7_ssm_backward(int B, int T, int D, int N, int G, wkv7_dtype in_d
         K.seg_g = (float *)take(round256((size_t)w.nseg * B * D * N * 4));
         K.seg_dt = (float *)take(round256((size_t)w.nseg * B * D * 4));
     }
-    P.nseg = w.nseg;
+    P.nseg = w.nseg, P.tiles = bwd_tiles(D, N, G);
     P.seg_len = (int)((((long long)T + w.nseg - 1) / w.nseg + kTile - 1) / kTile * kTile);
     K.dy = dy, K.g_f32 = g_dt == WKV7_F32, K.du = du, K.ddelta = ddelta, K.dz = dz, K.dstate0 = dstate0;
     cudaError_t e = cudaSuccess;
-    by_lanes(scan_lanes(N), [&](auto ln) {
-        constexpr int LN = decltype(ln)::value, EPT = kTile * scan_channels(LN) / kScanThreads, V = EPT < 8 ? EPT : 8;
-        if (in_dt == WKV7_F32) e = vec ? launch_bwd<float, LN, V>(K, dstateT, stream) : launch_bwd<float, LN, 1>(K, dstateT, stream);
-        else e = vec ? launch_bwd<bf16, LN, V>(K, dstateT, stream) : launch_bwd<bf16, LN, 1>(K, dstateT, stream);
+    by_pad(scan_pad(N), [&](auto np) {
+        constexpr int NP = decltype(np)::value;
+        if (in_dt == WKV7_F32) e = vec ? launch_bwd<float, NP, true>(K, dstateT, stream) : launch_bwd<float, NP, false>(K, dstateT, stream);
+        else e = vec ? launch_bwd<bf16, NP, true>(K, dstateT, stream) : launch_bwd<bf16, NP, false>(K, dstateT, stream);
     });
     if (e != cudaSuccess) return WKV7_ERR_CUDA;
     const long long n = (long long)B * T * G * N;

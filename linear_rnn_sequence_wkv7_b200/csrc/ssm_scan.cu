@@ -7,13 +7,20 @@
 // moves 8 bytes but takes 16 exponentials, and an SM makes 16 a cycle; the
 // state's update and readout (64 multiply-adds) stay below that.
 //
-// Mapping: a thread holds 2 channels x 4 n of the state in registers; LN = 2,
-// 4, 8 or 16 lanes side by side share a channel pair (N up to 8, 16, 32, 64,
-// the rest padded with zero rates and inputs, which keep a zero state at zero).
-// A tile of 16 tokens is prepared by the whole block (softplus and dt u once per
-// channel, not once per n) into shared memory, walked token by token, and its
-// outputs, joined over the LN lanes by shuffles, are gated by the threads that
-// loaded u and z.  Loads of the next tile are in flight meanwhile.
+// Mapping: a thread holds 4 (or 2) of a channel's n in registers, the lanes of a
+// channel side by side (N padded to 8, 16, 32 or 64 with zero rates and inputs,
+// which keep a zero state at zero).  A tile of 16 tokens is prepared by the whole
+// block (softplus and dt u once per channel, not once per n) into shared memory
+// and walked token by token, unrolled, so that the exponentials of later tokens
+// do not wait for the state.  Partial readouts go to shared memory lane by lane;
+// the threads that loaded u and z add them up, gate and store.  Loads of the next
+// tile are in flight meanwhile.
+//
+// Parallelism: one warp has 8 channels at N = 16 and needs about 50 instructions
+// for each of their tokens, four cycles apart when it is alone on its scheduler,
+// so blocks are small (16 channels).  Where even these leave schedulers with
+// fewer than three warps, a thread takes 2 n instead of 4 (twice the warps for
+// about a third more instructions).
 //
 // Few channels over many tokens: the state map of a stretch of tokens is
 // h -> exp(A sum dt) h + E, so the sequence is cut into segments: one pass takes
@@ -28,24 +35,26 @@ namespace wkv7 {
 namespace mixer {
 namespace {
 
-template <typename T, int LN, int V, bool Y>
-__global__ void __launch_bounds__(kScanThreads)
+template <typename T, int NP, int NPT, bool VEC, bool Y>
+__global__ void __launch_bounds__(scan_threads(NP, NPT))
 ssm_fwd_kernel(const ScanArgs P) {
-    constexpr int CC = scan_channels(LN), NP = 4 * LN;          // channels a block, padded N
-    constexpr int EPT = kTile * CC / kScanThreads, Q = EPT / V; // a thread's share of a tile, in Q vectors
-    constexpr int NB = kTile * NP / kScanThreads;               // and of B (and C)
+    constexpr int CC = scan_channels(NP), LN = NP / NPT, THREADS = CC * LN;
+    constexpr int EPT = kTile * CC / THREADS, V = VEC ? EPT : 1, Q = EPT / V;   // a thread's share of a tile
+    constexpr int IB = 2 * kTile * NP / 4, NB = (IB + THREADS - 1) / THREADS;   // quads of B, then of C
     constexpr bool PRECISE = sizeof(T) == 4;
-    __shared__ __align__(16) float s_dt[kTile][CC], s_du[kTile][CC], s_y[Y ? kTile : 1][CC];
-    __shared__ float4 s_B[kTile][LN], s_C[Y ? kTile : 1][LN];
+    __shared__ __align__(16) float2 s_dd[kTile][CC];                            // dt, dt u
+    __shared__ __align__(16) T s_BC[Y ? 2 : 1][kTile][NP];
+    using Sum = Planes<CC, LN>;
+    __shared__ __align__(16) float s_y[Y ? Sum::FLOATS : 1];
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long id = blockIdx.x;
-    const int tile_c = (int)(id % P.tiles);
-    id /= P.tiles;
-    const int g = (int)(id % P.G);
-    id /= P.G;
-    const long long b = id % P.B;
-    const int seg = (int)(id / P.B);
+    const int tid = threadIdx.x;
+    unsigned id = blockIdx.x;
+    const int tile_c = (int)(id % (unsigned)P.tiles);
+    id /= (unsigned)P.tiles;
+    const int g = (int)(id % (unsigned)P.G);
+    id /= (unsigned)P.G;
+    const long long b = id % (unsigned)P.B;
+    const int seg = (int)(id / (unsigned)P.B);
     const int c0 = g * P.Dg + tile_c * CC, c1 = (g + 1) * P.Dg;     // the block's channels [c0, min(c0 + CC, c1))
     int len = P.T;
     if (P.lens) len = min(max(__ldg(P.lens + b), 0), P.T);
@@ -66,25 +75,18 @@ ssm_fwd_kernel(const ScanArgs P) {
     const T *Bm = static_cast<const T *>(P.Bm) + b * P.b_bs + g * P.N;
     const T *Cm = static_cast<const T *>(P.Cm) + b * P.c_bs + g * P.N;
 
-    // and when it scans: channels cs, cs + 1 and n = ns .. ns + 3
-    const int nl = lane % LN, cl = (warp * (32 / LN) + lane / LN) * 2, cs = c0 + cl, ns = 4 * nl;
-    float2 a2[2][2], h[2][2];
+    // and when it scans: channel cs and n = ns .. ns + NPT - 1
+    const int nl = tid % LN, cl = tid / LN, cs = c0 + cl, ns = NPT * nl;
+    const bool mine = cs < c1;
+    float2 a2[NPT / 2], h[NPT / 2];
+    load_rates<NPT>(P.A + (size_t)cs * P.N, P.N, ns, mine, a2);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        float av[4], hv[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const bool in = cs + c < c1 && ns + n < P.N;
-            av[n] = in ? __ldg(P.A + (size_t)(cs + c) * P.N + ns + n) * kLog2e : 0.f;
-            hv[n] = (in && P.entry) ? P.entry[(((size_t)seg * P.B + b) * P.D + cs + c) * P.N + ns + n] : 0.f;
-        }
-        a2[c][0] = make_float2(av[0], av[1]), a2[c][1] = make_float2(av[2], av[3]);
-        h[c][0] = make_float2(hv[0], hv[1]), h[c][1] = make_float2(hv[2], hv[3]);
-    }
-    double sum0 = 0, sum1 = 0;                      // of dt, when summarising
+    for (int j = 0; j < NPT / 2; ++j) h[j] = make_float2(0.f, 0.f);
+    if (mine && P.entry) load_state<NPT>(P.entry + (((size_t)seg * P.B + b) * P.D + cs) * P.N, P.N, ns, h);
+    double sum = 0;                                 // of dt, when summarising
 
     Vec<T, V> nu[Q], nd[Q], nz[Q], cu[Q], cz[Q];
-    Vec<T, 1> nb[NB], nc[NB];
+    Quad<T, VEC> nb[NB];
     auto fetch = [&](int t) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
@@ -98,95 +100,63 @@ ssm_fwd_kernel(const ScanArgs P) {
         }
 #pragma unroll
         for (int q = 0; q < NB; ++q) {
-            const int e = tid + q * kScanThreads, tt = t + e / NP, n = e % NP;
-            nb[q].zero(), nc[q].zero();
-            if (tt < t1 && n < P.N) {
-                nb[q].load(Bm + tt * P.b_ts + n);
-                if (Y) nc[q].load(Cm + tt * P.c_ts + n);
-            }
+            const int e = tid + q * THREADS, tt = t + (e / (NP / 4)) % kTile, n = e % (NP / 4) * 4;
+            const bool c = e >= IB / 2, in = e < (Y ? IB : IB / 2) && tt < t1;
+            nb[q].load((c ? Cm + tt * P.c_ts : Bm + tt * P.b_ts) + n, in ? P.N - n : 0);
         }
     };
     auto prepare = [&](int t) {         // tokens behind t1: dt = dt u = B = 0 keep the state
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
             const int k = lt + q * (kTile / Q), ch = lc - c0;
+            const bool in = live && t + k < t1;
             float fu[V], fd[V];
             nu[q].get(fu), nd[q].get(fd);
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const float x = fd[i] + bias[i], dt = (live && t + k < t1) ? (P.softplus ? softplus(x) : x) : 0.f;
-                fu[i] = dt != 0.f ? dt * fu[i] : 0.f;
-                fd[i] = dt;
-            }
-            storev<V>(&s_dt[k][ch], fd);
-            storev<V>(&s_du[k][ch], fu);
+            for (int i = 0; i < V; ++i) fd[i] += bias[i];
+            if (P.softplus) softplus_all<PRECISE>(fd);
+#pragma unroll
+            for (int i = 0; i < V; ++i) fd[i] = in ? fd[i] : 0.f, fu[i] = in ? fd[i] * fu[i] : 0.f;
+            put_pairs<V>(&s_dd[k][ch], fd, fu);
             cu[q] = nu[q], cz[q] = nz[q];
         }
 #pragma unroll
         for (int q = 0; q < NB; ++q) {
-            const int e = tid + q * kScanThreads;
-            float f[1];
-            nb[q].get(f);
-            reinterpret_cast<float *>(s_B)[e] = f[0];
-            if (Y) {
-                nc[q].get(f);
-                reinterpret_cast<float *>(s_C)[e] = f[0];
-            }
+            const int e = tid + q * THREADS;
+            if (e < (Y ? IB : IB / 2)) nb[q].put(&s_BC[0][0][0] + 4 * e);
         }
     };
 
-    fetch(t0);
-    prepare(t0);
-    __syncthreads();
+    if (t0 < t1) {
+        fetch(t0);
+        prepare(t0);
+        __syncthreads();
+    }
     for (int t = t0; t < t1; t += kTile) {
         if (t + kTile < t1) fetch(t + kTile);
-        if (P.states) {
-            float *to = P.states + ((size_t)(b * P.nck + t / kTile) * P.D + cs) * P.N + ns;
+        if (P.states && mine)
+            store_state<NPT>(P.states + ((size_t)(b * P.nck + t / kTile) * P.D + cs) * P.N, P.N, ns, h);
+        float part = 0.f;
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
-                if (cs + c < c1) store_state(to + (size_t)c * P.N, P.N, ns, h[c]);
-        }
-        const int count = min(kTile, t1 - t);
-        float part0 = 0.f, part1 = 0.f;
-#pragma unroll 1
-        for (int k = 0; k < count; k += 2) {
-            float yv[4];
+        for (int k = 0; k < kTile; ++k) {
+            const float2 dd = s_dd[k][cl];
+            const float2 d2 = make_float2(dd.x, dd.x), w2 = make_float2(dd.y, dd.y);
+            float2 B[NPT / 2];
+            shared_n<NPT>(&s_BC[0][k][ns], B);
 #pragma unroll
-            for (int kk = 0; kk < 2; ++kk) {
-                const float2 dt = *reinterpret_cast<const float2 *>(&s_dt[k + kk][cl]);
-                const float2 du = *reinterpret_cast<const float2 *>(&s_du[k + kk][cl]);
-                const float4 B = s_B[k + kk][nl];
-                const float2 B0 = make_float2(B.x, B.y), B1 = make_float2(B.z, B.w);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float d = c ? dt.y : dt.x, w = c ? du.y : du.x;
-                    const float2 d2 = make_float2(d, d), w2 = make_float2(w, w);
-                    h[c][0] = __ffma2_rn(ex2(__fmul2_rn(d2, a2[c][0])), h[c][0], __fmul2_rn(w2, B0));
-                    h[c][1] = __ffma2_rn(ex2(__fmul2_rn(d2, a2[c][1])), h[c][1], __fmul2_rn(w2, B1));
-                }
-                if constexpr (Y) {
-                    const float4 C = s_C[k + kk][nl];
-                    const float2 C0 = make_float2(C.x, C.y), C1 = make_float2(C.z, C.w);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float2 p = __ffma2_rn(h[c][0], C0, __fmul2_rn(h[c][1], C1));
-                        yv[2 * kk + c] = p.x + p.y;
-                    }
-                } else {
-                    part0 += dt.x, part1 += dt.y;
-                }
-            }
-            if constexpr (Y) {          // 2 tokens x 2 channels over LN lanes
-                reduce_scatter<LN, 4>(yv, nl);
-                if constexpr (LN == 2) {
-                    s_y[k][cl + nl] = yv[0];
-                    s_y[k + 1][cl + nl] = yv[1];
-                } else if (nl < 4) {
-                    s_y[k + (nl >> 1)][cl + (nl & 1)] = yv[0];
-                }
+            for (int j = 0; j < NPT / 2; ++j)
+                h[j] = __ffma2_rn(ex2(__fmul2_rn(d2, a2[j])), h[j], __fmul2_rn(w2, B[j]));
+            if constexpr (Y) {
+                float2 C[NPT / 2];
+                shared_n<NPT>(&s_BC[Y ? 1 : 0][k][ns], C);
+                float2 p = __fmul2_rn(h[0], C[0]);
+                if constexpr (NPT == 4) p = __ffma2_rn(h[NPT / 2 - 1], C[NPT / 2 - 1], p);
+                Sum::put(s_y, k, cl, nl, p.x + p.y);
+            } else {
+                part += dd.x;
             }
         }
-        if constexpr (!Y) sum0 += part0, sum1 += part1;
+        if constexpr (!Y) sum += part;
         __syncthreads();
         if constexpr (Y) {
 #pragma unroll
@@ -195,9 +165,10 @@ ssm_fwd_kernel(const ScanArgs P) {
                 if (!live || t + k >= t1) continue;
                 float f[V], fu[V], fz[V];
                 cu[q].get(fu), cz[q].get(fz);
+                Sum::template sum<V>(s_y, k, lc - c0, f);
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    f[i] = fmaf(skip[i], fu[i], s_y[k][lc - c0 + i]);
+                    f[i] = fmaf(skip[i], fu[i], f[i]);
                     if (z) f[i] *= fz[i] * sigmoid<PRECISE>(fz[i]);
                 }
                 const size_t at = ((size_t)b * P.T + t + k) * P.D + lc;
@@ -208,18 +179,12 @@ ssm_fwd_kernel(const ScanArgs P) {
         if (t + kTile < t1) prepare(t + kTile);
         __syncthreads();
     }
-    if (seg == P.nseg - 1 && P.stateT)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-            if (cs + c < c1) store_state(P.stateT + ((size_t)b * P.D + cs + c) * P.N + ns, P.N, ns, h[c]);
+    if (!mine) return;
+    if (seg == P.nseg - 1 && P.stateT) store_state<NPT>(P.stateT + ((size_t)b * P.D + cs) * P.N, P.N, ns, h);
     if (!Y && P.seg_end) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-            if (cs + c >= c1) continue;
-            const size_t at = ((size_t)seg * P.B + b) * P.D + cs + c;
-            store_state(P.seg_end + at * P.N + ns, P.N, ns, h[c]);
-            if (nl == 0) P.seg_dt[at] = (float)(c ? sum1 : sum0);
-        }
+        const size_t at = ((size_t)seg * P.B + b) * P.D + cs;
+        store_state<NPT>(P.seg_end + at * P.N, P.N, ns, h);
+        if (nl == 0) P.seg_dt[at] = (float)sum;
     }
 }
 
@@ -281,7 +246,7 @@ ssm_step_kernel(const StepArgs P) {
     }
     const float u = to_f32(static_cast<const T *>(P.u)[b * P.u_bs + d]);
     const float x = to_f32(static_cast<const T *>(P.delta)[b * P.d_bs + d]) + (P.dt_bias ? __ldg(P.dt_bias + d) : 0.f);
-    const float dt = P.softplus ? softplus(x) : x, du = dt * u;
+    const float dt = P.softplus ? softplus<sizeof(T) == 4>(x) : x, du = dt * u;
     float y = 0.f;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
@@ -307,12 +272,20 @@ ssm_step_kernel(const StepArgs P) {
     }
 }
 
-template <typename T, int LN, bool Y>
-void launch_fwd(const ScanArgs &P, bool vec, cudaStream_t st) {
-    constexpr int CC = scan_channels(LN), EPT = kTile * CC / kScanThreads, V = EPT < 8 ? EPT : 8;
+template <typename T, int NP, int NPT, bool Y> void launch_fwd(const ScanArgs &P, bool vec, cudaStream_t st) {
     const unsigned grid = (unsigned)((long long)P.nseg * P.B * P.G * P.tiles);
-    if (vec) ssm_fwd_kernel<T, LN, V, Y><<<grid, kScanThreads, 0, st>>>(P);
-    else ssm_fwd_kernel<T, LN, 1, Y><<<grid, kScanThreads, 0, st>>>(P);
+    if (vec) ssm_fwd_kernel<T, NP, NPT, true, Y><<<grid, scan_threads(NP, NPT), 0, st>>>(P);
+    else ssm_fwd_kernel<T, NP, NPT, false, Y><<<grid, scan_threads(NP, NPT), 0, st>>>(P);
+}
+// Blocks, each of one schedule of warps: 2 n a thread where 4 would leave a
+// scheduler (four an SM) with fewer than three warps.  Padded to 64 a channel has
+// 16 lanes already.
+template <typename T, int NP, bool Y> void launch_fwd_npt(const ScanArgs &P, int sms, bool vec, cudaStream_t st) {
+    const long long warps = (long long)P.nseg * P.B * P.G * P.tiles * scan_threads(NP, 4) / 32;
+    if constexpr (NP < 64) {
+        if (warps < 12ll * sms) return launch_fwd<T, NP, 2, Y>(P, vec, st);
+    }
+    launch_fwd<T, NP, 4, Y>(P, vec, st);
 }
 
 }  // namespace
@@ -321,24 +294,24 @@ void launch_fwd(const ScanArgs &P, bool vec, cudaStream_t st) {
 // if that makes at least three of them (each token is then scanned twice), each
 // of at least 128 tokens.
 int ssm_segments(int B, int T, int D, int N, int G, int sms) {
-    const int CC = scan_channels(scan_lanes(N)), tiles = G > 0 ? (D / G + CC - 1) / CC : 0;
-    const long long blocks = (long long)B * G * tiles;
-    if (blocks <= 0 || sms <= 0) return 1;
-    const long long want = (long long)sms * 4 / blocks;
-    const long long most = T / 128;
+    const int NP = scan_pad(N), CC = scan_channels(NP), tiles = G > 0 ? (D / G + CC - 1) / CC : 0;
+    const long long warps = (long long)B * G * tiles * scan_threads(NP, 4) / 32;
+    if (warps <= 0 || sms <= 0) return 1;
+    const long long want = 16ll * sms / warps, most = T / 128;
     const long long s = want < most ? want : most;
     return s >= 3 ? (int)s : 1;
 }
 
 void ssm_fwd(const ScanArgs &P, wkv7_dtype dt, bool vec, bool y, cudaStream_t st) {
-    by_lanes(scan_lanes(P.N), [&](auto ln) {
-        constexpr int LN = decltype(ln)::value;
+    const int sms = sm_count();
+    by_pad(scan_pad(P.N), [&](auto np) {
+        constexpr int NP = decltype(np)::value;
         if (dt == WKV7_F32) {
-            if (y) launch_fwd<float, LN, true>(P, vec, st);
-            else launch_fwd<float, LN, false>(P, vec, st);
+            if (y) launch_fwd_npt<float, NP, true>(P, sms, vec, st);
+            else launch_fwd_npt<float, NP, false>(P, sms, vec, st);
         } else {
-            if (y) launch_fwd<bf16, LN, true>(P, vec, st);
-            else launch_fwd<bf16, LN, false>(P, vec, st);
+            if (y) launch_fwd_npt<bf16, NP, true>(P, sms, vec, st);
+            else launch_fwd_npt<bf16, NP, false>(P, sms, vec, st);
         }
     });
 }
@@ -374,18 +347,19 @@ wkv7_status ssm_dims(int B, int T, int D, int N, int G) {
     if (B < 0 || T < 0 || D < 0 || N <= 0 || G <= 0) return WKV7_ERR_INVALID_ARG;
     if (D % G != 0) return WKV7_ERR_INVALID_ARG;
     if (N > 64 || D > WKV7_SSM_MAX_D || T > kMaxTokens) return WKV7_ERR_UNSUPPORTED;
-    // blocks of the largest launch: a channel a block at most 16 channels wide, times the segments
-    const double chans = (double)B * (D + 16.0 * G);
-    if (chans * 64 / 256 > (double)kMaxGrid || chans > (double)kMaxGrid) return WKV7_ERR_UNSUPPORTED;
+    // a launch has at most 16 channels a block and 16 * 148 segments when that leaves SMs idle
+    if ((double)B * (D + 16.0 * G) > (double)kMaxGrid) return WKV7_ERR_UNSUPPORTED;
     return WKV7_OK;
 }
 
-// 16-byte vectors of 8 channels everywhere they are read or written
-bool ssm_vec(const ScanArgs &P, wkv7_dtype dt, const void *more, size_t more_size) {
-    const size_t al = 8 * dtype_size(dt) > 16 ? 16 : 8 * dtype_size(dt);
+// Vectors of up to 8 channels and of 4 n everywhere they are read or written
+bool ssm_vec(const ScanArgs &P, wkv7_dtype dt) {
+    const size_t quad = 4 * dtype_size(dt);
     const long long st = P.u_bs | P.u_ts | P.d_bs | P.d_ts | (P.z ? P.z_bs | P.z_ts : 0);
-    return P.Dg % 8 == 0 && st % 8 == 0 && aligned_to(P.u, al) && aligned_to(P.delta, al) && aligned_to(P.z, al) &&
-           aligned_to(P.y, 16) && aligned_to(more, more_size ? more_size : 1);
+    const long long sn = P.b_bs | P.b_ts | P.c_bs | P.c_ts;
+    return P.Dg % 8 == 0 && st % 8 == 0 && P.N % 4 == 0 && sn % 4 == 0 && aligned_to(P.u, 16) &&
+           aligned_to(P.delta, 16) && aligned_to(P.z, 16) && aligned_to(P.y, 16) && aligned_to(P.Bm, quad) &&
+           aligned_to(P.Cm, quad);
 }
 
 }  // namespace mixer
@@ -435,7 +409,7 @@ wkv7_status wkv7_ssm_forward(int B, int T, int D, int N, int G, wkv7_dtype in_dt
         return WKV7_ERR_INVALID_ARG;
     ScanArgs P{};
     P.B = B, P.T = T, P.D = D, P.N = N, P.G = G, P.Dg = D / G;
-    P.tiles = (P.Dg + scan_channels(scan_lanes(N)) - 1) / scan_channels(scan_lanes(N));
+    P.tiles = (P.Dg + scan_channels(scan_pad(N)) - 1) / scan_channels(scan_pad(N));
     P.u = u, P.u_bs = u_bs, P.u_ts = u_ts, P.delta = delta, P.d_bs = d_bs, P.d_ts = d_ts;
     P.z = z, P.z_bs = z_bs, P.z_ts = z_ts;
     P.Bm = Bm, P.b_bs = b_bs, P.b_ts = b_ts, P.Cm = Cm, P.c_bs = c_bs, P.c_ts = c_ts;
@@ -443,7 +417,7 @@ wkv7_status wkv7_ssm_forward(int B, int T, int D, int N, int G, wkv7_dtype in_dt
     P.y = y, P.y_f32 = y_dt == WKV7_F32, P.stateT = stateT, P.states = states, P.nck = (T + kTile - 1) / kTile;
     int nseg = ssm_segments(B, T, D, N, G, sm_count());
     if (nseg > 1 && (workspace == nullptr || workspace_bytes < ssm_segment_bytes(B, D, N, nseg))) nseg = 1;
-    ssm_fwd_all(P, state0, nseg, (char *)workspace, in_dt, ssm_vec(P, in_dt, nullptr, 0), true, stream);
+    ssm_fwd_all(P, state0, nseg, (char *)workspace, in_dt, ssm_vec(P, in_dt), true, stream);
     return launch_status();
 }
 
@@ -465,8 +439,8 @@ wkv7_status wkv7_ssm_step(int B, int D, int N, int G, wkv7_dtype in_dt, wkv7_dty
         return WKV7_ERR_INVALID_ARG;
     const StepArgs P{(long long)B * D, D, N, G, D / G, u, delta, Bm, Cm, z, u_bs, d_bs, b_bs, c_bs, z_bs, A, Dskip,
                      dt_bias, state, softplus, y};
-    by_lanes(scan_lanes(N), [&](auto ln) {
-        constexpr int LN = decltype(ln)::value;
+    by_pad(scan_pad(N), [&](auto np) {
+        constexpr int LN = decltype(np)::value / 4;
         const unsigned grid = (unsigned)((P.total * LN + 255) / 256);
         const bool vec = N == 4 * LN && aligned_to(A, 16);
 #define WKV7_STEP(I, O)                                                                 \

@@ -88,7 +88,7 @@ def norm_ref(x, res, w, eps):
     return s, rstd, s * rstd * w
 
 
-@pytest.mark.parametrize("rows,D", [(1, 1), (2, 7), (3, 128), (5, 130), (4, 1024), (2, 2560), (3, 4097), (2, 16384)])
+@pytest.mark.parametrize("rows,D", [(1, 1), (2, 7), (3, 128), (5, 130), (4, 1024), (700, 2048), (2, 2560), (3, 4097), (2, 16384)])
 @pytest.mark.parametrize("dtype,res", [("f32", None), ("f32", "f32"), ("bf16", "bf16"), ("bf16", "f32"), ("f32", "bf16"),
                                        ("bf16", None)])
 def test_rmsnorm_forward(cuda_device, rows, D, dtype, res):
@@ -130,7 +130,7 @@ def test_rmsnorm_zero_row_and_in_place(cuda_device):
     assert torch.isinf(ssm.rmsnorm_forward(x[1:2], w, eps=0.0).rstd).all()
 
 
-@pytest.mark.parametrize("rows,D", [(1, 1), (3, 130), (300, 256), (5, 2560), (2, 9000)])
+@pytest.mark.parametrize("rows,D", [(1, 1), (3, 130), (300, 256), (5, 2560), (3, 2048), (2, 9000)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("kept", ["act8", "sum"])
 def test_rmsnorm_backward(cuda_device, rows, D, dtype, kept):
