@@ -5,6 +5,8 @@ import glob
 import os
 import subprocess
 import sys
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,7 +18,7 @@ NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC,-fvisibility=hidden", "-shared",
+    "-Xcompiler", "-fPIC,-fvisibility=hidden",
     "--expt-relaxed-constexpr",
 ]
 
@@ -33,14 +35,25 @@ def needs_build() -> bool:
     return any(os.path.getmtime(s) > mtime for s in _sources())
 
 
+# Translation units: the WKV7 kernels share one __device__ status word and are
+# compiled together; the state-space mixer's files stand alone.
+UNITS = ("libwkv7.cu", "act8.cu", "rmsnorm.cu", "conv.cu", "ssm_scan.cu", "ssm_bwd.cu")
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and not needs_build():
         return LIB_PATH
     tmp = LIB_PATH + f".tmp{os.getpid()}"
-    cmd = [NVCC, *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC, os.path.join(CSRC, "libwkv7.cu"), "-o", tmp]
-    if verbose:
-        cmd.insert(1, "-Xptxas=-v")
-    subprocess.check_call(cmd)
+    flags = NVCC_FLAGS + (["-Xptxas=-v"] if verbose else []) + ["-I", INCLUDE, "-I", CSRC]
+    with tempfile.TemporaryDirectory() as objects:
+        def unit(name):
+            obj = os.path.join(objects, name + ".o")
+            subprocess.check_call([NVCC, *flags, "-c", os.path.join(CSRC, name), "-o", obj])
+            return obj
+
+        with ThreadPoolExecutor(len(UNITS)) as pool:
+            objs = list(pool.map(unit, UNITS))
+        subprocess.check_call([NVCC, *NVCC_FLAGS, "-shared", *objs, "-o", tmp])
     os.replace(tmp, LIB_PATH)
     return LIB_PATH
 

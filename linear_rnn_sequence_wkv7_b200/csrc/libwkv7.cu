@@ -11,8 +11,3 @@
 #include "bwd_noalloc.cu"
 #include "fwd_host.cu"
 #include "timemix.cu"
-#include "act8.cu"
-#include "rmsnorm.cu"
-#include "conv.cu"
-#include "ssm_scan.cu"
-#include "ssm_bwd.cu"

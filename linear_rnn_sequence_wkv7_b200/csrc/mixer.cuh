@@ -93,11 +93,18 @@ template <int V> __device__ __forceinline__ void storev(bf16 *p, const float (&f
     }
 }
 
+// BYTES (4, 8 or 16) to shared memory without passing through registers; zeros when !in
+template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const void *src, bool in) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES),
+                 "r"(in ? BYTES : 0)
+                 : "memory");
+}
+
 // ---- functions ------------------------------------------------------------------
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float rcp(float x) {

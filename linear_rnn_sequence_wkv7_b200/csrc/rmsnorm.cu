@@ -43,9 +43,6 @@ __device__ __forceinline__ void batch_load(const void *p, wkv7_dtype dt, long lo
 // (cp.async) by the thread that reads them, so no barrier is needed.  A slot is
 // four values, 8 bytes or (WIDE) 16; slots behind the row's end stay zero.
 constexpr int kAhead = 4;
-template <int BYTES> __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
-}
 template <int MB, bool WIDE, int TENSORS> struct Ring {
     static constexpr int SLOT = WIDE ? 16 : 8;
     unsigned char *base;
@@ -64,7 +61,7 @@ template <int MB, bool WIDE, int TENSORS> struct Ring {
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
                 const int c = lane_channel<true>(blk0 + m * step, lane, 0);
-                if (c < D) copy_async<4 * (int)sizeof(t)>(smem_u32(slot(stage, tensor, m)), row + c);
+                if (c < D) copy_async<4 * (int)sizeof(t)>(slot(stage, tensor, m), row + c, true);
             }
         });
     }

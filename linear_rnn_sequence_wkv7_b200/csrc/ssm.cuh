@@ -11,11 +11,13 @@ namespace mixer {
 
 constexpr int kTile = 16;           // tokens a tile, and between saved states
 
-// N padded to 8, 16, 32 or 64.  A thread holds NPT (4 or 2) of a channel's n; the
-// NP / NPT lanes of a channel sit side by side.
+// N padded to 8, 16, 32 or 64; a thread holds 4 n of TC channels
 inline int scan_pad(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 64; }
-__host__ __device__ constexpr int scan_channels(int NP) { return NP == 8 ? 32 : 16; }      // of a block
-__host__ __device__ constexpr int scan_threads(int NP, int NPT) { return scan_channels(NP) * NP / NPT; }
+__host__ __device__ constexpr int scan_channels(int NP) { return NP == 8 ? 32 : NP == 64 ? 8 : 16; }      // of a block
+__host__ __device__ constexpr int scan_threads(int NP, int TC) { return scan_channels(NP) * NP / (4 * TC); }
+
+// blocks of 2 scan_threads an SM that the registers must leave room for
+__host__ __device__ constexpr int scan_blocks(int NP, int TC) { return 20 * 16 / scan_threads(NP, TC); }
 
 template <typename F> void by_pad(int NP, F &&f) {
     if (NP == 8) f(std::integral_constant<int, 8>{});
@@ -70,41 +72,34 @@ template <typename T, bool VEC> struct Quad {
     }
 };
 
-// A thread's numbers of a channel's state row, n = ns .. ns + NPT - 1; N need not be a multiple of NPT
-template <int NPT> __device__ __forceinline__ void store_state(float *row, int N, int ns, const float2 (&h)[NPT / 2]) {
-    if (N % NPT == 0) {
-        if (ns >= N) return;
-        if constexpr (NPT == 4) *reinterpret_cast<float4 *>(row + ns) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
-        else *reinterpret_cast<float2 *>(row + ns) = h[0];
+// A thread's numbers of a channel's state row, n = ns .. ns + 3; N need not be a multiple of 4
+__device__ __forceinline__ void store_state(float *row, int N, int ns, const float2 (&h)[2]) {
+    if ((N & 3) == 0) {
+        if (ns < N) *reinterpret_cast<float4 *>(row + ns) = make_float4(h[0].x, h[0].y, h[1].x, h[1].y);
     } else {
 #pragma unroll
-        for (int n = 0; n < NPT; ++n)
+        for (int n = 0; n < 4; ++n)
             if (ns + n < N) row[ns + n] = (n & 1) ? h[n / 2].y : h[n / 2].x;
     }
 }
-template <int NPT> __device__ __forceinline__ void load_state(const float *row, int N, int ns, float2 (&h)[NPT / 2]) {
-    if (N % NPT == 0) {
-#pragma unroll
-        for (int j = 0; j < NPT / 2; ++j) h[j] = make_float2(0.f, 0.f);
-        if (ns >= N) return;
-        if constexpr (NPT == 4) {
-            const float4 v = *reinterpret_cast<const float4 *>(row + ns);
-            h[0] = make_float2(v.x, v.y), h[1] = make_float2(v.z, v.w);
-        } else {
-            h[0] = *reinterpret_cast<const float2 *>(row + ns);
+__device__ __forceinline__ void load_state(const float *row, int N, int ns, float2 (&h)[2]) {
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    if ((N & 3) == 0) {
+        if (ns < N) {
+            const float4 q = *reinterpret_cast<const float4 *>(row + ns);
+            v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
         }
     } else {
-        float v[NPT];
 #pragma unroll
-        for (int n = 0; n < NPT; ++n) v[n] = ns + n < N ? row[ns + n] : 0.f;
-#pragma unroll
-        for (int j = 0; j < NPT / 2; ++j) h[j] = make_float2(v[2 * j], v[2 * j + 1]);
+        for (int n = 0; n < 4; ++n)
+            if (ns + n < N) v[n] = row[ns + n];
     }
+    h[0] = make_float2(v[0], v[1]), h[1] = make_float2(v[2], v[3]);
 }
 // The rates of a thread's n in units of log 2 (0 for the padding, which keeps a zero state at zero)
-template <int NPT> __device__ __forceinline__ void load_rates(const float *row, int N, int ns, bool live, float2 (&a)[NPT / 2]) {
+__device__ __forceinline__ void load_rates(const float *row, int N, int ns, bool live, float2 (&a)[2]) {
 #pragma unroll
-    for (int j = 0; j < NPT / 2; ++j) {
+    for (int j = 0; j < 2; ++j) {
         const int n = ns + 2 * j;
         a[j].x = (live && n < N) ? __ldg(row + n) * kLog2e : 0.f;
         a[j].y = (live && n + 1 < N) ? __ldg(row + n + 1) * kLog2e : 0.f;
@@ -114,24 +109,16 @@ template <int NPT> __device__ __forceinline__ void load_rates(const float *row, 
 // the SM's shared memory for every 4 bytes a lane, broadcast or not, and at 16
 // bytes each for B and C that would be the scan's bound.
 // A thread's n of a token:
-template <int NPT> __device__ __forceinline__ void shared_n(const float *p, float2 (&v)[NPT / 2]) {
-    if constexpr (NPT == 4) {
-        const float4 q = *reinterpret_cast<const float4 *>(p);
-        v[0] = make_float2(q.x, q.y), v[1] = make_float2(q.z, q.w);
-    } else {
-        v[0] = *reinterpret_cast<const float2 *>(p);
-    }
+__device__ __forceinline__ void shared_n(const float *p, float2 (&v)[2]) {
+    const float4 q = *reinterpret_cast<const float4 *>(p);
+    v[0] = make_float2(q.x, q.y), v[1] = make_float2(q.z, q.w);
 }
 __device__ __forceinline__ float2 bf16_pair(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
-template <int NPT> __device__ __forceinline__ void shared_n(const bf16 *p, float2 (&v)[NPT / 2]) {
-    if constexpr (NPT == 4) {
-        const uint2 q = *reinterpret_cast<const uint2 *>(p);
-        v[0] = bf16_pair(q.x), v[1] = bf16_pair(q.y);
-    } else {
-        v[0] = bf16_pair(*reinterpret_cast<const uint32_t *>(p));
-    }
+__device__ __forceinline__ void shared_n(const bf16 *p, float2 (&v)[2]) {
+    const uint2 q = *reinterpret_cast<const uint2 *>(p);
+    v[0] = bf16_pair(q.x), v[1] = bf16_pair(q.y);
 }
 
 // (a_i, b_i) of V channels in a row
@@ -150,6 +137,9 @@ template <int V> __device__ __forceinline__ void put_pairs(float2 *to, const flo
 template <int CC, int LN> struct Planes {
     static constexpr int PS = CC + 32 / LN, RS = LN * PS + (CC == 16 ? 16 : 0), FLOATS = kTile * RS;
     static __device__ __forceinline__ void put(float *s, int k, int ch, int nl, float v) { s[k * RS + nl * PS + ch] = v; }
+    template <int TC> static __device__ __forceinline__ void put(float *s, int k, int ch, int nl, const float (&v)[TC]) {
+        storev<TC>(s + k * RS + nl * PS + ch, v);
+    }
     template <int V> static __device__ __forceinline__ void sum(const float *s, int k, int ch, float (&out)[V]) {
         const float *p = s + k * RS + ch;
         if constexpr (V % 4 == 0) {

@@ -54,7 +54,7 @@ struct BwdArgs {
 
 // A segment's own adjoint (from zero behind it) and sum of dt
 template <typename T, int NP, bool VEC>
-__global__ void __launch_bounds__(scan_threads(NP, 4))
+__global__ void __launch_bounds__(scan_threads(NP, 1))
 ssm_bwd_summary_kernel(const BwdArgs K) {
     const ScanArgs &P = K.f;
     constexpr int CC = scan_channels(NP), LN = NP / 4, THREADS = CC * LN;
@@ -82,7 +82,7 @@ ssm_bwd_summary_kernel(const BwdArgs K) {
     const T *Cm = static_cast<const T *>(P.Cm) + b * P.c_bs + g * P.N;
     const int nl = tid % LN, cl = tid / LN, cs = c0 + cl, ns = 4 * nl;
     float2 a2[2], w[2];
-    load_rates<4>(P.A + (size_t)cs * P.N, P.N, ns, cs < c1, a2);
+    load_rates(P.A + (size_t)cs * P.N, P.N, ns, cs < c1, a2);
     w[0] = w[1] = make_float2(0.f, 0.f);
     float bias[V];
 #pragma unroll
@@ -138,7 +138,7 @@ ssm_bwd_summary_kernel(const BwdArgs K) {
         for (int k = kTile - 1; k >= 0; --k) {
             const float2 dd = s_dd[k][cl], d2 = make_float2(dd.x, dd.x), e2 = make_float2(dd.y, dd.y);
             float2 C[2];
-            shared_n<4>(&s_C[k][ns], C);
+            shared_n(&s_C[k][ns], C);
 #pragma unroll
             for (int j = 0; j < 2; ++j) w[j] = __fmul2_rn(ex2(__fmul2_rn(d2, a2[j])), __ffma2_rn(e2, C[j], w[j]));
             part += dd.x;
@@ -148,7 +148,7 @@ ssm_bwd_summary_kernel(const BwdArgs K) {
     }
     if (cs >= c1) return;
     const size_t at = ((size_t)seg * P.B + b) * P.D + cs;
-    store_state<4>(K.seg_g + at * P.N, P.N, ns, w);
+    store_state(K.seg_g + at * P.N, P.N, ns, w);
     if (nl == 0) K.seg_dt[at] = (float)sum;
 }
 
@@ -243,10 +243,10 @@ ssm_bwd_kernel(const BwdArgs K) {
     const int nl = tid % LN, cl = tid / LN, cs = c0 + cl, ns = 4 * nl, cg = lane / LN, order = cg & 3;
     const bool mine = cs < c1;
     float2 a2[2], w[2];             // rates (log2), adjoint carried to the token before; by slots
-    load_rates<4>(P.A + (size_t)cs * P.N, P.N, ns, mine, a2);
+    load_rates(P.A + (size_t)cs * P.N, P.N, ns, mine, a2);
     permute(a2, order);
     w[0] = w[1] = make_float2(0.f, 0.f);
-    if (mine && K.exit) load_state<4>(K.exit + (((size_t)seg * P.B + b) * P.D + cs) * P.N, P.N, ns, w);
+    if (mine && K.exit) load_state(K.exit + (((size_t)seg * P.B + b) * P.D + cs) * P.N, P.N, ns, w);
     permute(w, order);
     for (int i = 0; i < 2 * V; ++i) s_acc[i * THREADS + tid] = 0.f;
 #pragma unroll
@@ -301,7 +301,7 @@ ssm_bwd_kernel(const BwdArgs K) {
             for (int p = 0; p < 4; ++p) nb[q].put(to + p * NP, p);
         }
         h0[0] = h0[1] = make_float2(0.f, 0.f);
-        if (mine) load_state<4>(P.states + ((size_t)(b * P.nck + t / kTile) * P.D + cs) * P.N, P.N, ns, h0);
+        if (mine) load_state(P.states + ((size_t)(b * P.nck + t / kTile) * P.D + cs) * P.N, P.N, ns, h0);
         permute(h0, order);
     };
 
@@ -322,7 +322,7 @@ ssm_bwd_kernel(const BwdArgs K) {
         auto advance = [&](int k, const float2 (&from)[2], float2 (&to)[2]) {
             const float2 dd = s_dd[k][cl], d2 = make_float2(dd.x, dd.x), v2 = make_float2(dd.y, dd.y);
             float2 B[2];
-            shared_n<4>(&s_BC[0][k][order][ns], B);
+            shared_n(&s_BC[0][k][order][ns], B);
 #pragma unroll
             for (int j = 0; j < 2; ++j) to[j] = __ffma2_rn(ex2(__fmul2_rn(d2, a2[j])), from[j], __fmul2_rn(v2, B[j]));
         };
@@ -341,8 +341,8 @@ ssm_bwd_kernel(const BwdArgs K) {
             const float e = s_ds[k][cl];
             const float2 e2 = make_float2(e, e);
             float2 B[2], C[2], gg[2], dB[2], dC[2], q[2];
-            shared_n<4>(&s_BC[0][k][order][ns], B);
-            shared_n<4>(&s_BC[1][k][order][ns], C);
+            shared_n(&s_BC[0][k][order][ns], B);
+            shared_n(&s_BC[1][k][order][ns], C);
             if (z) {
                 const float2 y = __ffma2_rn(h[i][1], C[1], __fmul2_rn(h[i][0], C[0]));
                 Sum::put(s_y, k, cl, nl, y.x + y.y);
@@ -451,13 +451,13 @@ ssm_bwd_kernel(const BwdArgs K) {
     const size_t part = (size_t)seg * P.B + b;
     if (mine) {
         permute(w, order);
-        if (seg == 0 && K.dstate0) store_state<4>(K.dstate0 + ((size_t)b * P.D + cs) * P.N, P.N, ns, w);
+        if (seg == 0 && K.dstate0) store_state(K.dstate0 + ((size_t)b * P.D + cs) * P.N, P.N, ns, w);
         float v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = s_dA[2 * i * THREADS + tid] + s_dA[(2 * i + 1) * THREADS + tid];
         float2 v2[2] = {make_float2(v[0], v[1]), make_float2(v[2], v[3])};
         permute(v2, order);
-        store_state<4>(K.dA + (part * P.D + cs) * P.N, P.N, ns, v2);
+        store_state(K.dA + (part * P.D + cs) * P.N, P.N, ns, v2);
     }
     // dD and ddt_bias: the threads that loaded the same channels, in order
     __syncthreads();
@@ -491,7 +491,7 @@ cudaError_t launch_bwd(const BwdArgs &K, const float *dstateT, cudaStream_t st) 
     M.exit = dstateT;
     if (P.nseg > 1) {
         const long long blocks = (long long)P.nseg * P.B * P.G * ((P.Dg + scan_channels(NP) - 1) / scan_channels(NP));
-        ssm_bwd_summary_kernel<T, NP, VEC><<<(unsigned)blocks, scan_threads(NP, 4), 0, st>>>(K);
+        ssm_bwd_summary_kernel<T, NP, VEC><<<(unsigned)blocks, scan_threads(NP, 1), 0, st>>>(K);
         const long long total = (long long)P.B * P.D * P.N;
         ssm_bwd_chain_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(total, P.N, P.nseg, P.A, P.D, dstateT,
                                                                              K.seg_dt, K.seg_g);

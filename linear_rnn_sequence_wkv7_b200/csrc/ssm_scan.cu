@@ -7,25 +7,27 @@
 // moves 8 bytes but takes 16 exponentials, and an SM makes 16 a cycle; the
 // state's update and readout (64 multiply-adds) stay below that.
 //
-// Mapping: a thread holds 4 (or 2) of a channel's n in registers, the lanes of a
-// channel side by side (N padded to 8, 16, 32 or 64 with zero rates and inputs,
-// which keep a zero state at zero).  A tile of 16 tokens is prepared by the whole
-// block (softplus and dt u once per channel, not once per n) into shared memory
-// and walked token by token, unrolled, so that the exponentials of later tokens
-// do not wait for the state.  Partial readouts go to shared memory lane by lane;
-// the threads that loaded u and z add them up, gate and store.  Loads of the next
-// tile are in flight meanwhile.
+// Mapping: a thread of the scanning half of a block holds 4 n of one or two
+// channels in registers, the lanes of a channel side by side (N padded to 8, 16,
+// 32 or 64 with zero rates and inputs, which keep a zero state at zero).  It walks
+// tiles of 16 tokens, unrolled, with the exponentials of four tokens under way
+// while the four before them run through the state, and leaves its part of C . h
+// in shared memory, lane by lane.  The other half of the block copies tiles in
+// (cp.async, three ahead), prepares the next tile (softplus and dt u once per
+// channel, not once per n) and adds up, gates and stores the one before, so that
+// neither kind of work waits for the other's latencies.
 //
-// Parallelism: one warp has 8 channels at N = 16 and needs about 50 instructions
-// for each of their tokens, four cycles apart when it is alone on its scheduler,
-// so blocks are small (16 channels).  Where even these leave schedulers with
-// fewer than three warps, a thread takes 2 n instead of 4 (twice the warps for
-// about a third more instructions).
+// 8 x 4096 tokens x 2048 channels, N = 16, bf16 in and out: 480 us, 2.2 times the
+// exponentials alone; the schedulers issue 57% of cycles, the exponentials' pipe
+// is busy for 65%.  One warp for both kinds of work took 511 us, B and C in fp32
+// in shared memory or 8 tokens ahead no less.
 //
 // Few channels over many tokens: the state map of a stretch of tokens is
 // h -> exp(A sum dt) h + E, so the sequence is cut into segments: one pass takes
 // every segment's E (from a zero state, no output) and sum dt, a chain gives the
-// entry states, and the outputs come from a second pass over all segments.
+// entry states, and the outputs come from a second pass over all segments (1 x
+// 65536 tokens x 2048 channels: 1.58 ms in 18 segments; one piece has 128 warps
+// for 148 SMs).
 #include <type_traits>
 
 #include "mixer.cuh"
@@ -35,19 +37,68 @@ namespace wkv7 {
 namespace mixer {
 namespace {
 
-template <typename T, int NP, int NPT, bool VEC, bool Y>
-__global__ void __launch_bounds__(scan_threads(NP, NPT))
+constexpr int kRing = 4;            // tiles of raw inputs on their way or in use
+
+// Shared memory of a block
+template <typename T, int NP, bool Y> struct ScanShared {
+    static constexpr int CC = scan_channels(NP), NIN = Y ? 3 : 2;
+    float2 dd[2][kTile][CC];                        // dt, dt u
+    T in[kRing][NIN][kTile][CC];                    // u, delta, z
+    T BC[kRing][Y ? 2 : 1][kTile][NP];
+    float y[Y ? 2 : 1][Y ? Planes<CC, NP / 4>::FLOATS : 4];     // C . h, lane by lane
+};
+
+// V elements to shared memory: asynchronously, or through a register where they are two bytes
+template <int V, typename T> __device__ __forceinline__ void copy_in(T *to, const T *from) {
+    if constexpr (V * sizeof(T) >= 4) copy_async<V * (int)sizeof(T)>(to, from, true);
+    else *to = *from;
+}
+template <int V, typename T> __device__ __forceinline__ void shared_get(const T *p, float (&f)[V]) {
+    Vec<T, V> v;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(v.w) / 4; ++i)
+        v.w[i] = sizeof(T) * V < 4 ? *reinterpret_cast<const uint16_t *>(p) : 0;
+    if constexpr (sizeof(v.w) == 16 && sizeof(T) * V == 16) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p);
+        v.w[0] = q.x, v.w[1] = q.y, v.w[2] = q.z, v.w[3] = q.w;
+    } else if constexpr (sizeof(T) * V == 8) {
+        const uint2 q = *reinterpret_cast<const uint2 *>(p);
+        v.w[0] = q.x, v.w[1] = q.y;
+    } else if constexpr (sizeof(T) * V == 4) {
+        v.w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+    v.get(f);
+}
+
+template <int THREADS> __device__ __forceinline__ int scan_flip() {
+    if constexpr (THREADS >= 256) return 0;
+    __shared__ int flip;
+    if (threadIdx.x == 0) {
+        uint32_t slot;
+        asm volatile("mov.u32 %0, %%warpid;" : "=r"(slot));
+        flip = (slot >> 2) & 1;
+    }
+    __syncthreads();
+    return flip;
+}
+
+template <typename T, int NP, int TC, bool VEC, bool Y>
+__global__ void __launch_bounds__(2 * scan_threads(NP, TC), scan_blocks(NP, TC))
 ssm_fwd_kernel(const ScanArgs P) {
-    constexpr int CC = scan_channels(NP), LN = NP / NPT, THREADS = CC * LN;
-    constexpr int EPT = kTile * CC / THREADS, V = VEC ? EPT : 1, Q = EPT / V;   // a thread's share of a tile
+    constexpr int CC = scan_channels(NP), LN = NP / 4, THREADS = scan_threads(NP, TC);     // of each kind
+    constexpr int EPT = kTile * CC / THREADS, V = VEC ? (EPT < 4 ? EPT : 4) : 1, Q = EPT / V;   // a thread's share of a tile
     constexpr int IB = 2 * kTile * NP / 4, NB = (IB + THREADS - 1) / THREADS;   // quads of B, then of C
     constexpr bool PRECISE = sizeof(T) == 4;
-    __shared__ __align__(16) float2 s_dd[kTile][CC];                            // dt, dt u
-    __shared__ __align__(16) T s_BC[Y ? 2 : 1][kTile][NP];
     using Sum = Planes<CC, LN>;
-    __shared__ __align__(16) float s_y[Y ? Sum::FLOATS : 1];
+    using S = ScanShared<T, NP, Y>;
+    constexpr int NIN = S::NIN;
+    extern __shared__ __align__(16) unsigned char scan_smem[];
+    S &sh = *reinterpret_cast<S *>(scan_smem);
+    auto &s_dd = sh.dd;
+    auto &s_in = sh.in;
+    auto &s_BC = sh.BC;
+    auto &s_y = sh.y;
 
-    const int tid = threadIdx.x;
     unsigned id = blockIdx.x;
     const int tile_c = (int)(id % (unsigned)P.tiles);
     id /= (unsigned)P.tiles;
@@ -60,131 +111,213 @@ ssm_fwd_kernel(const ScanArgs P) {
     if (P.lens) len = min(max(__ldg(P.lens + b), 0), P.T);
     const int t0 = (int)min((long long)seg * P.seg_len, (long long)len);
     const int t1 = (int)min((long long)t0 + P.seg_len, (long long)len);
+    const int nt = (t1 - t0 + kTile - 1) / kTile;
 
-    // this thread's channels when it loads: V in a row, the same in each of its Q vectors
-    const int lc = c0 + (tid % (CC / V)) * V, lt = tid / (CC / V);
-    const bool live = lc < c1;
-    float bias[V], skip[V];
+    // Which half of the block scans: a warp's place among the SM's four schedulers goes with its slot, so
+    // blocks of fewer than four warps a half take turns, by the slot that the block got.  (Only the
+    // balance hangs on it.)
+    const int flip = scan_flip<2 * THREADS>();
+    const int tid = threadIdx.x < THREADS ? threadIdx.x : threadIdx.x - THREADS;
+    if ((threadIdx.x >= THREADS) != (flip != 0)) {
+        // ---- the other half: tiles in, outputs out.  V channels in a row, the same in each of Q vectors.
+        const int ch = (tid % (CC / V)) * V, lt = tid / (CC / V);
+        const bool live = c0 + ch < c1;
+        const int lc = live ? c0 + ch : c0;         // channels behind the group load others' values and store nothing
+        float bias[V], skip[V];
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        bias[i] = (live && P.dt_bias) ? __ldg(P.dt_bias + lc + i) : 0.f;
-        skip[i] = (Y && live && P.Dskip) ? __ldg(P.Dskip + lc + i) : 0.f;
-    }
-    const T *u = static_cast<const T *>(P.u) + b * P.u_bs + lc, *de = static_cast<const T *>(P.delta) + b * P.d_bs + lc;
-    const T *z = (Y && P.z) ? static_cast<const T *>(P.z) + b * P.z_bs + lc : nullptr;
-    const T *Bm = static_cast<const T *>(P.Bm) + b * P.b_bs + g * P.N;
-    const T *Cm = static_cast<const T *>(P.Cm) + b * P.c_bs + g * P.N;
-
-    // and when it scans: channel cs and n = ns .. ns + NPT - 1
-    const int nl = tid % LN, cl = tid / LN, cs = c0 + cl, ns = NPT * nl;
-    const bool mine = cs < c1;
-    float2 a2[NPT / 2], h[NPT / 2];
-    load_rates<NPT>(P.A + (size_t)cs * P.N, P.N, ns, mine, a2);
+        for (int i = 0; i < V; ++i) {
+            bias[i] = P.dt_bias ? __ldg(P.dt_bias + lc + i) : 0.f;
+            skip[i] = (Y && P.Dskip) ? __ldg(P.Dskip + lc + i) : 0.f;
+        }
+        const bool gate = Y && P.z != nullptr;
+        constexpr int QT = kTile / Q;               // tokens between a thread's vectors
+        const T *pu = static_cast<const T *>(P.u) + b * P.u_bs + (t0 + lt) * P.u_ts + lc;
+        const T *pd = static_cast<const T *>(P.delta) + b * P.d_bs + (t0 + lt) * P.d_ts + lc;
+        const T *pz = gate ? static_cast<const T *>(P.z) + b * P.z_bs + (t0 + lt) * P.z_ts + lc : nullptr;
+        const T *Bm = static_cast<const T *>(P.Bm) + b * P.b_bs + t0 * P.b_ts + g * P.N;
+        const T *Cm = static_cast<const T *>(P.Cm) + b * P.c_bs + t0 * P.c_ts + g * P.N;
+        const size_t y0 = ((size_t)b * P.T + t0 + lt) * P.D + lc;
+        float *yf = static_cast<float *>(P.y) + (Y ? y0 : 0);
+        bf16 *yh = static_cast<bf16 *>(P.y) + (Y ? y0 : 0);
+        // Tile j's inputs, as they are, into ring slot j mod kRing: u, delta, z for this thread, B and C for the scan
+        auto fetch = [&](int j) {
+            if (j < nt) {
+                const int t = t0 + j * kTile, slot = j % kRing;
+                const bool full = t + kTile <= t1;      // uniform
 #pragma unroll
-    for (int j = 0; j < NPT / 2; ++j) h[j] = make_float2(0.f, 0.f);
-    if (mine && P.entry) load_state<NPT>(P.entry + (((size_t)seg * P.B + b) * P.D + cs) * P.N, P.N, ns, h);
-    double sum = 0;                                 // of dt, when summarising
-
-    Vec<T, V> nu[Q], nd[Q], nz[Q], cu[Q], cz[Q];
-    Quad<T, VEC> nb[NB];
-    auto fetch = [&](int t) {
+                for (int q = 0; q < Q; ++q) {
+                    const int k = lt + q * QT;
+                    if (!full && t + k >= t1) continue;
+                    copy_in<V>(&s_in[slot][0][k][ch], pu + q * QT * P.u_ts);
+                    copy_in<V>(&s_in[slot][1][k][ch], pd + q * QT * P.d_ts);
+                    if (gate) copy_in<V>(&s_in[slot][NIN - 1][k][ch], pz + q * QT * P.z_ts);
+                }
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const int tt = t + lt + q * (kTile / Q);
-            nu[q].zero(), nd[q].zero(), nz[q].zero();
-            if (live && tt < t1) {
-                nu[q].load(u + tt * P.u_ts);
-                nd[q].load(de + tt * P.d_ts);
-                if (z) nz[q].load(z + tt * P.z_ts);
+                for (int q = 0; q < NB; ++q) {
+                    const int e = tid + q * THREADS, k = (e / (NP / 4)) % kTile, n = e % (NP / 4) * 4;
+                    if (e >= (Y ? IB : IB / 2)) break;
+                    const bool in = full || t + k < t1;
+                    T *to = &s_BC[slot][0][0][0] + 4 * e;
+                    const T *from = (Y && e >= IB / 2 ? Cm + k * P.c_ts : Bm + k * P.b_ts) + n;
+                    if constexpr (VEC) copy_async<4 * (int)sizeof(T)>(to, from, in && n < P.N);
+                    else {
+                        Quad<T, false> v;
+                        v.load(from, in ? P.N - n : 0);
+                        v.put(to);
+                    }
+                }
+                pu += kTile * P.u_ts, pd += kTile * P.d_ts, Bm += kTile * P.b_ts, Cm += kTile * P.c_ts;
+                if (gate) pz += kTile * P.z_ts;
             }
-        }
-#pragma unroll
-        for (int q = 0; q < NB; ++q) {
-            const int e = tid + q * THREADS, tt = t + (e / (NP / 4)) % kTile, n = e % (NP / 4) * 4;
-            const bool c = e >= IB / 2, in = e < (Y ? IB : IB / 2) && tt < t1;
-            nb[q].load((c ? Cm + tt * P.c_ts : Bm + tt * P.b_ts) + n, in ? P.N - n : 0);
-        }
-    };
-    auto prepare = [&](int t) {         // tokens behind t1: dt = dt u = B = 0 keep the state
-#pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            const int k = lt + q * (kTile / Q), ch = lc - c0;
-            const bool in = live && t + k < t1;
-            float fu[V], fd[V];
-            nu[q].get(fu), nd[q].get(fd);
-#pragma unroll
-            for (int i = 0; i < V; ++i) fd[i] += bias[i];
-            if (P.softplus) softplus_all<PRECISE>(fd);
-#pragma unroll
-            for (int i = 0; i < V; ++i) fd[i] = in ? fd[i] : 0.f, fu[i] = in ? fd[i] * fu[i] : 0.f;
-            put_pairs<V>(&s_dd[k][ch], fd, fu);
-            cu[q] = nu[q], cz[q] = nz[q];
-        }
-#pragma unroll
-        for (int q = 0; q < NB; ++q) {
-            const int e = tid + q * THREADS;
-            if (e < (Y ? IB : IB / 2)) nb[q].put(&s_BC[0][0][0] + 4 * e);
-        }
-    };
-
-    if (t0 < t1) {
-        fetch(t0);
-        prepare(t0);
-        __syncthreads();
-    }
-    for (int t = t0; t < t1; t += kTile) {
-        if (t + kTile < t1) fetch(t + kTile);
-        if (P.states && mine)
-            store_state<NPT>(P.states + ((size_t)(b * P.nck + t / kTile) * P.D + cs) * P.N, P.N, ns, h);
-        float part = 0.f;
-#pragma unroll
-        for (int k = 0; k < kTile; ++k) {
-            const float2 dd = s_dd[k][cl];
-            const float2 d2 = make_float2(dd.x, dd.x), w2 = make_float2(dd.y, dd.y);
-            float2 B[NPT / 2];
-            shared_n<NPT>(&s_BC[0][k][ns], B);
-#pragma unroll
-            for (int j = 0; j < NPT / 2; ++j)
-                h[j] = __ffma2_rn(ex2(__fmul2_rn(d2, a2[j])), h[j], __fmul2_rn(w2, B[j]));
-            if constexpr (Y) {
-                float2 C[NPT / 2];
-                shared_n<NPT>(&s_BC[Y ? 1 : 0][k][ns], C);
-                float2 p = __fmul2_rn(h[0], C[0]);
-                if constexpr (NPT == 4) p = __ffma2_rn(h[NPT / 2 - 1], C[NPT / 2 - 1], p);
-                Sum::put(s_y, k, cl, nl, p.x + p.y);
-            } else {
-                part += dd.x;
-            }
-        }
-        if constexpr (!Y) sum += part;
-        __syncthreads();
-        if constexpr (Y) {
+            cp_async_commit();
+        };
+        auto prepare = [&](int j) {     // tokens behind t1: dt = dt u = B = 0 keep the state
+            const int t = t0 + j * kTile, slot = j % kRing;
+            const bool full = t + kTile <= t1;
 #pragma unroll
             for (int q = 0; q < Q; ++q) {
-                const int k = lt + q * (kTile / Q);
-                if (!live || t + k >= t1) continue;
-                float f[V], fu[V], fz[V];
-                cu[q].get(fu), cz[q].get(fz);
-                Sum::template sum<V>(s_y, k, lc - c0, f);
+                const int k = lt + q * QT;
+                float fu[V], fd[V];
+                shared_get<V>(&s_in[slot][0][k][ch], fu);
+                shared_get<V>(&s_in[slot][1][k][ch], fd);
 #pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    f[i] = fmaf(skip[i], fu[i], f[i]);
-                    if (z) f[i] *= fz[i] * sigmoid<PRECISE>(fz[i]);
+                for (int i = 0; i < V; ++i) fd[i] += bias[i];
+                if (P.softplus) softplus_all<PRECISE>(fd);
+#pragma unroll
+                for (int i = 0; i < V; ++i) fu[i] *= fd[i];
+                if (!full && t + k >= t1) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) fd[i] = fu[i] = 0.f;
                 }
-                const size_t at = ((size_t)b * P.T + t + k) * P.D + lc;
-                if (P.y_f32) storev<V>(static_cast<float *>(P.y) + at, f);
-                else storev<V>(static_cast<bf16 *>(P.y) + at, f);
+                put_pairs<V>(&s_dd[j & 1][k][ch], fd, fu);
+            }
+        };
+        auto finish = [&](int j) {
+            if constexpr (Y) {
+                const int t = t0 + j * kTile, slot = j % kRing;
+                const bool full = t + kTile <= t1;
+#pragma unroll
+                for (int q = 0; q < Q; ++q) {
+                    const int k = lt + q * QT;
+                    float f[V], fu[V], fz[V];
+                    shared_get<V>(&s_in[slot][0][k][ch], fu);
+                    if (gate) shared_get<V>(&s_in[slot][NIN - 1][k][ch], fz);
+                    Sum::template sum<V>(s_y[j & 1], k, ch, f);
+#pragma unroll
+                    for (int i = 0; i < V; ++i) {
+                        f[i] = fmaf(skip[i], fu[i], f[i]);
+                        if (gate) f[i] *= fz[i] * sigmoid<PRECISE>(fz[i]);
+                    }
+                    if (live && (full || t + k < t1)) {
+                        if (P.y_f32) storev<V>(yf + (size_t)q * QT * P.D, f);
+                        else storev<V>(yh + (size_t)q * QT * P.D, f);
+                    }
+                }
+                yf += (size_t)kTile * P.D, yh += (size_t)kTile * P.D;
+            }
+        };
+        // While tile j is in the scan: tile j - 1 goes out, which frees its slot for tile j + 3, and tile j + 1
+        // is prepared.  A slot's u, delta and z are read by the thread that copied them; the barrier shows B and
+        // C to the scan.
+        fetch(0), fetch(1), fetch(2);
+        cp_async_wait<2>();
+        if (nt > 0) prepare(0);
+        __syncthreads();
+        for (int j = 0; j < nt; ++j) {
+            if (j > 0) finish(j - 1);
+            fetch(j + 3);
+            cp_async_wait<2>();
+            if (j + 1 < nt) prepare(j + 1);
+            __syncthreads();
+        }
+        if (nt > 0) finish(nt - 1);
+        return;
+    }
+
+    // ---- the scan: channels cs .. cs + TC - 1 and n = ns .. ns + 3
+    const int nl = tid % LN, cl = tid / LN * TC, cs = c0 + cl, ns = 4 * nl;
+    float2 a2[TC][2], h[TC][2];
+#pragma unroll
+    for (int c = 0; c < TC; ++c) {
+        const bool mine = cs + c < c1;
+        load_rates(P.A + (size_t)(cs + c) * P.N, P.N, ns, mine, a2[c]);
+        h[c][0] = h[c][1] = make_float2(0.f, 0.f);
+        if (mine && P.entry) load_state(P.entry + (((size_t)seg * P.B + b) * P.D + cs + c) * P.N, P.N, ns, h[c]);
+    }
+    double sum[TC] = {};                            // of dt, when summarising
+    __syncthreads();
+    for (int j = 0; j < nt; ++j) {
+        const int buf = j & 1, slot = j % kRing;
+        if (P.states) {
+#pragma unroll
+            for (int c = 0; c < TC; ++c)
+                if (cs + c < c1)
+                    store_state(P.states + ((size_t)(b * P.nck + t0 / kTile + j) * P.D + cs + c) * P.N, P.N, ns, h[c]);
+        }
+        float part[TC] = {};
+        // A group's decays and inputs are on their way while the group before it runs through the state
+        constexpr int GT = 4;
+        float2 a[2][GT][TC][2], in[2][GT][TC][2];
+        auto ready = [&](int k0, float2 (&av)[GT][TC][2], float2 (&bv)[GT][TC][2]) {
+#pragma unroll
+            for (int i = 0; i < GT; ++i) {
+                float dt[TC], du[TC];
+                if constexpr (TC == 2) {
+                    const float4 q = *reinterpret_cast<const float4 *>(&s_dd[buf][k0 + i][cl]);
+                    dt[0] = q.x, du[0] = q.y, dt[TC - 1] = q.z, du[TC - 1] = q.w;
+                } else {
+                    const float2 q = s_dd[buf][k0 + i][cl];
+                    dt[0] = q.x, du[0] = q.y;
+                }
+                float2 B[2];
+                shared_n(&s_BC[slot][0][k0 + i][ns], B);
+#pragma unroll
+                for (int c = 0; c < TC; ++c) {
+                    const float2 d2 = make_float2(dt[c], dt[c]), w2 = make_float2(du[c], du[c]);
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                        av[i][c][m] = ex2(__fmul2_rn(d2, a2[c][m])), bv[i][c][m] = __fmul2_rn(w2, B[m]);
+                    if constexpr (!Y) part[c] += dt[c];
+                }
+            }
+        };
+        ready(0, a[0], in[0]);
+#pragma unroll
+        for (int k = 0; k < kTile; k += GT) {
+            if (k + GT < kTile) ready(k + GT, a[(k / GT + 1) & 1], in[(k / GT + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < GT; ++i) {
+                float2 C[2];
+                if constexpr (Y) shared_n(&s_BC[slot][Y ? 1 : 0][k + i][ns], C);
+                float y[TC];
+#pragma unroll
+                for (int c = 0; c < TC; ++c) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+                        h[c][m] = __ffma2_rn(a[(k / GT) & 1][i][c][m], h[c][m], in[(k / GT) & 1][i][c][m]);
+                    if constexpr (Y) {
+                        const float2 p = __ffma2_rn(h[c][1], C[1], __fmul2_rn(h[c][0], C[0]));
+                        y[c] = p.x + p.y;
+                    }
+                }
+                if constexpr (Y) Sum::template put<TC>(s_y[buf], k + i, cl, nl, y);
             }
         }
-        if (t + kTile < t1) prepare(t + kTile);
+        if constexpr (!Y) {
+#pragma unroll
+            for (int c = 0; c < TC; ++c) sum[c] += part[c];
+        }
         __syncthreads();
     }
-    if (!mine) return;
-    if (seg == P.nseg - 1 && P.stateT) store_state<NPT>(P.stateT + ((size_t)b * P.D + cs) * P.N, P.N, ns, h);
-    if (!Y && P.seg_end) {
-        const size_t at = ((size_t)seg * P.B + b) * P.D + cs;
-        store_state<NPT>(P.seg_end + at * P.N, P.N, ns, h);
-        if (nl == 0) P.seg_dt[at] = (float)sum;
+#pragma unroll
+    for (int c = 0; c < TC; ++c) {
+        if (cs + c >= c1) continue;
+        if (seg == P.nseg - 1 && P.stateT) store_state(P.stateT + ((size_t)b * P.D + cs + c) * P.N, P.N, ns, h[c]);
+        if (!Y && P.seg_end) {
+            const size_t at = ((size_t)seg * P.B + b) * P.D + cs + c;
+            store_state(P.seg_end + at * P.N, P.N, ns, h[c]);
+            if (nl == 0) P.seg_dt[at] = (float)sum[c];
+        }
     }
 }
 
@@ -272,32 +405,34 @@ ssm_step_kernel(const StepArgs P) {
     }
 }
 
-template <typename T, int NP, int NPT, bool Y> void launch_fwd(const ScanArgs &P, bool vec, cudaStream_t st) {
+template <typename T, int NP, int TC, bool Y> void launch_fwd(const ScanArgs &P, bool vec, cudaStream_t st) {
     const unsigned grid = (unsigned)((long long)P.nseg * P.B * P.G * P.tiles);
-    if (vec) ssm_fwd_kernel<T, NP, NPT, true, Y><<<grid, scan_threads(NP, NPT), 0, st>>>(P);
-    else ssm_fwd_kernel<T, NP, NPT, false, Y><<<grid, scan_threads(NP, NPT), 0, st>>>(P);
+    constexpr int threads = 2 * scan_threads(NP, TC);
+    constexpr size_t smem = sizeof(ScanShared<T, NP, Y>);
+    auto kernel = vec ? ssm_fwd_kernel<T, NP, TC, true, Y> : ssm_fwd_kernel<T, NP, TC, false, Y>;
+    if (smem > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    kernel<<<grid, threads, smem, st>>>(P);
 }
-// Blocks, each of one schedule of warps: 2 n a thread where 4 would leave a
-// scheduler (four an SM) with fewer than three warps.  Padded to 64 a channel has
-// 16 lanes already.
-template <typename T, int NP, bool Y> void launch_fwd_npt(const ScanArgs &P, int sms, bool vec, cudaStream_t st) {
-    const long long warps = (long long)P.nseg * P.B * P.G * P.tiles * scan_threads(NP, 4) / 32;
-    if constexpr (NP < 64) {
-        if (warps < 12ll * sms) return launch_fwd<T, NP, 2, Y>(P, vec, st);
-    }
-    launch_fwd<T, NP, 4, Y>(P, vec, st);
+// Two channels a thread halve the loads of B and C and the instructions around
+// them; one channel a thread makes twice the warps.  At N = 16 and 8 x 4096 tokens
+// x 2048 channels (7 scanning warps an SM at two): 482 us at two, 503 us at one;
+// below 6 warps an SM at two the schedulers run dry.
+template <typename T, int NP, bool Y> void launch_fwd_tc(const ScanArgs &P, int sms, bool vec, cudaStream_t st) {
+    const long long warps = (long long)P.nseg * P.B * P.G * P.tiles * scan_threads(NP, 2) / 32;
+    if (warps < 6ll * sms) return launch_fwd<T, NP, 1, Y>(P, vec, st);
+    launch_fwd<T, NP, 2, Y>(P, vec, st);
 }
 
 }  // namespace
 
-// Segments of a forward over B sequences: enough that its blocks fill the SMs,
-// if that makes at least three of them (each token is then scanned twice), each
-// of at least 128 tokens.
+// Segments of a forward over B sequences: 16 scanning warps an SM at two channels
+// a thread, if that makes at least three segments (each token is then scanned
+// twice), each of at least 128 tokens.
 int ssm_segments(int B, int T, int D, int N, int G, int sms) {
     const int NP = scan_pad(N), CC = scan_channels(NP), tiles = G > 0 ? (D / G + CC - 1) / CC : 0;
-    const long long warps = (long long)B * G * tiles * scan_threads(NP, 4) / 32;
+    const long long warps = (long long)B * G * tiles * scan_threads(NP, 1) / 32;
     if (warps <= 0 || sms <= 0) return 1;
-    const long long want = 16ll * sms / warps, most = T / 128;
+    const long long want = 32ll * sms / warps, most = T / 128;
     const long long s = want < most ? want : most;
     return s >= 3 ? (int)s : 1;
 }
@@ -307,11 +442,11 @@ void ssm_fwd(const ScanArgs &P, wkv7_dtype dt, bool vec, bool y, cudaStream_t st
     by_pad(scan_pad(P.N), [&](auto np) {
         constexpr int NP = decltype(np)::value;
         if (dt == WKV7_F32) {
-            if (y) launch_fwd_npt<float, NP, true>(P, sms, vec, st);
-            else launch_fwd_npt<float, NP, false>(P, sms, vec, st);
+            if (y) launch_fwd_tc<float, NP, true>(P, sms, vec, st);
+            else launch_fwd_tc<float, NP, false>(P, sms, vec, st);
         } else {
-            if (y) launch_fwd_npt<bf16, NP, true>(P, sms, vec, st);
-            else launch_fwd_npt<bf16, NP, false>(P, sms, vec, st);
+            if (y) launch_fwd_tc<bf16, NP, true>(P, sms, vec, st);
+            else launch_fwd_tc<bf16, NP, false>(P, sms, vec, st);
         }
     });
 }
