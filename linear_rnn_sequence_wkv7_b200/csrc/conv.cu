@@ -20,8 +20,9 @@ void sum_parts(long long parts, long long cols, const float *partial, float *out
 namespace {
 
 constexpr int kConvWarps = 4;       // forward: warps a block, each a run of its own
-constexpr int kConvRun = 32;        // tokens a run
-constexpr int kConvAhead = 8;       // tokens whose loads are issued together
+constexpr int kConvMinRun = 16;
+constexpr int kConvGroup = 4;       // tokens worked on together, unrolled
+constexpr int kConvRing = 4;        // groups on their way or in use
 
 // Four channels of one token, and the scale when they are codes
 template <typename T, bool VEC> struct Token {
@@ -44,20 +45,118 @@ template <typename T, bool VEC> struct Token {
     }
 };
 
+// Tokens on their way to a warp: kConvRing groups of kConvGroup, each lane's four
+// channels in a slot of its own, copied (cp.async) by the lane that reads them.
+// Where an element is too narrow for that (not VEC and not fp32), one group ahead
+// in registers.
+template <typename T, bool VEC> struct Stream {
+    static constexpr bool ASYNC = VEC || sizeof(T) == 4;
+    static constexpr int SLOT = 4 * (int)sizeof(T);
+    static constexpr int BYTES = ASYNC ? kConvRing * kConvGroup * (32 * SLOT + (sizeof(T) == 1 ? 4 : 0)) : 0;   // a warp
+    unsigned char *base;
+    Token<T, VEC> next[ASYNC ? 1 : kConvGroup];
+    __device__ __forceinline__ unsigned char *slot(int i, int lane) const { return base + (i * 32 + lane) * SLOT; }
+    __device__ __forceinline__ float *scale(int i) const {
+        return reinterpret_cast<float *>(base + kConvRing * kConvGroup * 32 * SLOT) + i;
+    }
+    // group g of tokens from `row` on, `left` of them there (the others count as zero)
+    __device__ __forceinline__ void fetch(int g, const T *row, long long ts, const float *scales, int nblk, int left,
+                                          int blk, int lane, int D) {
+#pragma unroll
+        for (int k = 0; k < kConvGroup; ++k) {
+            if constexpr (ASYNC) {
+                unsigned char *to = slot((g % kConvRing) * kConvGroup + k, lane);
+                if constexpr (VEC) {
+                    const int c = lane_channel<true>(blk, lane, 0);
+                    const bool in = k < left && c < D;
+                    copy_async<SLOT>(to, in ? row + k * ts + c : row, in);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int c = lane_channel<false>(blk, lane, i);
+                        const bool in = k < left && c < D;
+                        copy_async<(int)sizeof(T) < 4 ? 4 : (int)sizeof(T)>(to + 4 * i, in ? row + k * ts + c : row, in);
+                    }
+                }
+            } else {
+                next[k].zero();
+                if (k < left) next[k].load(row + k * ts, scales + (long long)k * nblk, blk, lane, D);
+            }
+        }
+        if constexpr (ASYNC && sizeof(T) == 1) {
+            if (lane < kConvGroup) {
+                const bool in = lane < left;
+                copy_async<4>(scale((g % kConvRing) * kConvGroup + lane), in ? scales + (long long)lane * nblk : scales, in);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int g, int lane, float (&v)[kConvGroup][4]) const {
+#pragma unroll
+        for (int k = 0; k < kConvGroup; ++k) {
+            if constexpr (ASYNC) {
+                const int i = (g % kConvRing) * kConvGroup + k;
+                Vec<T, 4> r;
+                const uint32_t *w = reinterpret_cast<const uint32_t *>(slot(i, lane));
+                if constexpr (SLOT == 16) {
+                    const uint4 q = *reinterpret_cast<const uint4 *>(w);
+                    r.w[0] = q.x, r.w[1] = q.y, r.w[2] = q.z, r.w[3] = q.w;
+                } else if constexpr (SLOT == 8) {
+                    const uint2 q = *reinterpret_cast<const uint2 *>(w);
+                    r.w[0] = q.x, r.w[1] = q.y;
+                } else {
+                    r.w[0] = w[0];
+                }
+                r.get(v[k]);
+                if constexpr (sizeof(T) == 1) {
+                    const float f = *scale(i);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) v[k][c] *= f;
+                }
+            } else {
+                next[k].get(v[k]);
+            }
+        }
+    }
+};
+
 template <bool VEC, typename T>
 __device__ __forceinline__ void load4c(const T *row, int blk, int lane, int D, float (&f)[4]) {
     row_load<VEC>(row, blk, lane, D, f);
 }
+// Four channels as two pairs: one packed instruction works on a pair
+__device__ __forceinline__ void pairs(const float (&f)[4], float2 (&p)[2]) {
+    p[0] = make_float2(f[0], f[1]), p[1] = make_float2(f[2], f[3]);
+}
 
+// A lane's weights and biases; with vector accesses its 4 W weights are one stretch of memory
 template <int W, bool VEC>
 __device__ __forceinline__ void load_params(const float *weight, const float *bias, int blk, int lane, int D,
-                                            float (&w)[W][4], float (&b)[4]) {
+                                            float2 (&w)[W][2], float2 (&b)[2]) {
+    float f[4], v[4 * W];
+    if constexpr (VEC) {
+        const int c = lane_channel<true>(blk, lane, 0);
+        const float4 zero = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int c = lane_channel<VEC>(blk, lane, i);
-        b[i] = (bias && c < D) ? __ldg(bias + c) : 0.f;
+        for (int j = 0; j < W; ++j) {
+            const float4 q = c < D ? __ldg(reinterpret_cast<const float4 *>(weight + (size_t)c * W) + j) : zero;
+            v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
+        }
+        const float4 q = (bias && c < D) ? __ldg(reinterpret_cast<const float4 *>(bias + c)) : zero;
+        f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
+    } else {
 #pragma unroll
-        for (int j = 0; j < W; ++j) w[j][i] = c < D ? __ldg(weight + (size_t)c * W + j) : 0.f;
+        for (int i = 0; i < 4; ++i) {
+            const int c = lane_channel<false>(blk, lane, i);
+            f[i] = (bias && c < D) ? __ldg(bias + c) : 0.f;
+#pragma unroll
+            for (int j = 0; j < W; ++j) v[i * W + j] = c < D ? __ldg(weight + (size_t)c * W + j) : 0.f;
+        }
+    }
+    pairs(f, b);
+#pragma unroll
+    for (int j = 0; j < W; ++j) {
+        w[j][0] = make_float2(v[j], v[W + j]);
+        w[j][1] = make_float2(v[2 * W + j], v[3 * W + j]);
     }
 }
 
@@ -73,12 +172,12 @@ struct ConvFwd {
     void *y, *state_out;
     uint8_t *codes;
     float *scales;
-    int runs;
+    int runs, run;                  // runs of `run` tokens
 };
 
 // ST: the state's type (x's, or y's when x is codes).  SAVE: x's codes go out too.
 template <typename T, typename ST, typename YT, int W, bool VEC, bool SAVE>
-__global__ void __launch_bounds__(32 * kConvWarps)
+__global__ void __launch_bounds__(32 * kConvWarps, VEC && !SAVE ? 6 : 4)
 conv_fwd_kernel(const ConvFwd P) {
     constexpr bool PRECISE = sizeof(YT) == 4;
     const int lane = threadIdx.x & 31, D = P.D, nblk = (D + kBlk - 1) / kBlk;
@@ -90,7 +189,7 @@ conv_fwd_kernel(const ConvFwd P) {
     if (b >= P.B) return;
     int len = P.T;
     if (P.lens) len = min(max(__ldg(P.lens + b), 0), P.T);
-    const int t0 = run * kConvRun, t1 = min(t0 + kConvRun, len);
+    const int t0 = min(run * P.run, len), t1 = min(t0 + P.run, len);
     const T *x = static_cast<const T *>(P.x) + b * P.x_bs;
     const ST *state = static_cast<const ST *>(P.state);
     const float *xs = sizeof(T) == 1 ? P.x_scales + b * P.T * nblk + blk : nullptr;
@@ -118,48 +217,79 @@ conv_fwd_kernel(const ConvFwd P) {
         }
     }
     if (t0 >= t1) return;
-    float w[W][4], bias[4];
+    const long long row0 = b * P.T + t0;
+    const T *px = x + t0 * P.x_ts;
+    const float *ps = xs + (long long)t0 * nblk;
+    YT *py = static_cast<YT *>(P.y) + row0 * D;
+    uint8_t *pc = SAVE ? P.codes + row0 * D : nullptr;
+    float *pq = SAVE ? P.scales + row0 * nblk + blk : nullptr;
+    extern __shared__ __align__(16) unsigned char conv_smem[];
+    Stream<T, VEC> in{conv_smem + (threadIdx.x >> 5) * Stream<T, VEC>::BYTES};
+    constexpr bool ASYNC = Stream<T, VEC>::ASYNC;
+    auto fetch = [&](int g) {
+        const int t = t0 + g * kConvGroup;
+        if (t < t1) in.fetch(g, px + (long long)g * kConvGroup * P.x_ts, P.x_ts, ps + (long long)g * kConvGroup * nblk, nblk,
+                             t1 - t, blk, lane, D);
+        if constexpr (ASYNC) cp_async_commit();
+    };
+    fetch(0);
+    if constexpr (ASYNC) {
+#pragma unroll
+        for (int g = 1; g < kConvRing - 1; ++g) fetch(g);
+    }
+    float2 w[W][2], bias[2], h[W - 1][2];           // h: the last W - 1 inputs, oldest first
     load_params<W, VEC>(P.weight, P.bias, blk, lane, D, w, bias);
-    float h[W - 1][4];                              // the last W - 1 inputs, oldest first
 #pragma unroll
-    for (int j = 0; j < W - 1; ++j) past(t0 - (W - 1) + j, h[j]);
-    YT *y = static_cast<YT *>(P.y) + b * P.T * (long long)D;
-    Token<T, VEC> next[kConvAhead];
+    for (int j = 0; j < W - 1; ++j) {
+        float f[4];
+        past(t0 - (W - 1) + j, f);
+        pairs(f, h[j]);
+    }
+    for (int g = 0, t = t0; t < t1; ++g, t += kConvGroup) {
+        const int left = t1 - t;
+        float v[kConvGroup][4];
+        if constexpr (ASYNC) {
+            if (sizeof(T) == 1) __syncwarp();       // the scales of the group that goes were read by all lanes
+            fetch(g + kConvRing - 1);
+            cp_async_wait<kConvRing - 1>();
+            if (sizeof(T) == 1) __syncwarp();       // and those of this one copied by some
+            in.get(g, lane, v);
+        } else {
+            in.get(g, lane, v);
+            fetch(g + 1);
+        }
+        if constexpr (SAVE) {
+            uint32_t q[kConvGroup];
+            float scale[kConvGroup];
+            act8_encode_all(v, q, scale);
 #pragma unroll
-    for (int k = 0; k < kConvAhead; ++k)
-        if (t0 + k < t1) next[k].load(x + (t0 + k) * P.x_ts, xs + (long long)(t0 + k) * nblk, blk, lane, D);
-    for (int t = t0; t < t1; t += kConvAhead) {
-        Token<T, VEC> now[kConvAhead];
-#pragma unroll
-        for (int k = 0; k < kConvAhead; ++k) now[k] = next[k];
-#pragma unroll
-        for (int k = 0; k < kConvAhead; ++k)
-            if (t + kConvAhead + k < t1)
-                next[k].load(x + (t + kConvAhead + k) * P.x_ts, xs + (long long)(t + kConvAhead + k) * nblk, blk, lane, D);
-#pragma unroll
-        for (int k = 0; k < kConvAhead; ++k) {
-            if (t + k >= t1) break;
-            float v[4], o[4];
-            now[k].get(v);
-            if constexpr (SAVE) {
-                uint32_t q;
-                const float scale = act8_encode(v, q);
-                const long long r = b * P.T + t + k;
-                row_store_codes<VEC>(P.codes + r * D, blk, lane, D, q);
-                if (lane == 0) P.scales[r * nblk + blk] = scale;
+            for (int k = 0; k < kConvGroup; ++k) {
+                if (k >= left) break;
+                row_store_codes<VEC>(pc + (long long)k * D, blk, lane, D, q[k]);
+                if (lane == 0) pq[(long long)k * nblk] = scale[k];
             }
+            pc += (long long)kConvGroup * D;
+            pq += (long long)kConvGroup * nblk;
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float p = fmaf(w[W - 1][i], v[i], bias[i]);
+        for (int k = 0; k < kConvGroup; ++k) {
+            float2 now[2];
+            float o[4];
+            pairs(v[k], now);
 #pragma unroll
-                for (int j = W - 2; j >= 0; --j) p = fmaf(w[j][i], h[j][i], p);
-                o[i] = P.silu ? p * sigmoid<PRECISE>(p) : p;
+            for (int i = 0; i < 2; ++i) {
+                float2 p = __ffma2_rn(w[W - 1][i], now[i], bias[i]);
+#pragma unroll
+                for (int j = W - 2; j >= 0; --j) p = __ffma2_rn(w[j][i], h[j][i], p);
+                if (P.silu) p = __fmul2_rn(p, sigmoid2<PRECISE>(p));
+                o[2 * i] = p.x, o[2 * i + 1] = p.y;
 #pragma unroll
                 for (int j = 0; j < W - 2; ++j) h[j][i] = h[j + 1][i];
-                h[W - 2][i] = v[i];
+                h[W - 2][i] = now[i];
             }
-            row_store<VEC>(y + (long long)(t + k) * D, blk, lane, D, o);
+            if (k < left) row_store<VEC>(py + (long long)k * D, blk, lane, D, o);
         }
+        py += (long long)kConvGroup * D;
     }
 }
 
@@ -187,8 +317,7 @@ conv_step_kernel(long long total, int D, const T *__restrict__ x, long long x_bs
 }
 
 constexpr int kConvBwdWarps = 4;    // backward: runs a block, joined in shared memory
-constexpr int kConvBwdRun = 64;     // tokens a run
-constexpr int kConvBwdAhead = 4;
+constexpr int kConvBwdRun = 64;    // tokens a run
 
 struct ConvBwd {
     int B, T, D;
@@ -212,6 +341,9 @@ __global__ void __launch_bounds__(32 * kConvBwdWarps, VEC ? 3 : 2)
 conv_bwd_kernel(const ConvBwd P) {
     constexpr bool PRECISE = sizeof(GT) == 4;
     __shared__ float part[kConvBwdWarps][W + 1][kBlk];
+    extern __shared__ __align__(16) unsigned char conv_smem[];
+    Stream<T, VEC> xin{conv_smem + (threadIdx.x >> 5) * Stream<T, VEC>::BYTES};
+    Stream<DT, VEC> gin{conv_smem + kConvBwdWarps * Stream<T, VEC>::BYTES + (threadIdx.x >> 5) * Stream<DT, VEC>::BYTES};
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = P.D, nblk = (D + kBlk - 1) / kBlk;
     const int blk = (int)(blockIdx.x % nblk);
     const long long rest = blockIdx.x / nblk;
@@ -224,83 +356,123 @@ conv_bwd_kernel(const ConvBwd P) {
     const DT *dy = static_cast<const DT *>(P.dy) + b * P.T * (long long)D;
     GT *dx = static_cast<GT *>(P.dx) + b * P.T * (long long)D;
     const float *xs = sizeof(T) == 1 ? P.x_scales + b * P.T * nblk + blk : nullptr;
-    float w[W][4], bias[4], dw[W][4], db[4];
+    float2 w[W][2], bias[2], dw[W][2], db[2];
     load_params<W, VEC>(P.weight, P.bias, blk, lane, D, w, bias);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        db[i] = 0.f;
+    for (int i = 0; i < 2; ++i) {
+        db[i] = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int j = 0; j < W; ++j) dw[j][i] = 0.f;
+        for (int j = 0; j < W; ++j) dw[j][i] = make_float2(0.f, 0.f);
     }
     if (t0 < t1) {
-        float h[W][4], dp[W][4];                    // x and dp at t - W + 1 .. t
+        float2 h[W][2], dp[W][2];                   // x and dp at t - W + 1 .. t
 #pragma unroll
         for (int j = 0; j < W; ++j) {
             const int t = t0 - W + j;               // shifted once before the first token
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dp[j][i] = h[j][i] = 0.f;
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
             if (j > 0 && t >= 0) {
                 Token<T, VEC> k;
                 k.load(x + t * P.x_ts, xs + (long long)t * nblk, blk, lane, D);
-                k.get(h[j]);
+                k.get(f);
             } else if (j > 0 && state) {
-                load4c<VEC>(state + (b * (W - 1) + (t + W - 1)) * D, blk, lane, D, h[j]);
+                load4c<VEC>(state + (b * (W - 1) + (t + W - 1)) * D, blk, lane, D, f);
             }
+            pairs(f, h[j]);
+            dp[j][0] = dp[j][1] = make_float2(0.f, 0.f);
         }
-        const int end = t1 + W - 1;
-        const int last = min(end, P.T);             // tokens behind the sequence count as zero
-        Token<T, VEC> xn[kConvBwdAhead];
-        Token<DT, VEC> gn[kConvBwdAhead];
-        auto fetch = [&](int tt) {
+        const int end = t1 + W - 1, last = min(end, P.T);       // tokens behind the sequence count as zero
+        constexpr bool ASYNC = Stream<T, VEC>::ASYNC && Stream<DT, VEC>::ASYNC;
+        constexpr bool MIXED = !ASYNC && (Stream<T, VEC>::ASYNC || Stream<DT, VEC>::ASYNC);
+        static_assert(!MIXED || !VEC, "vector accesses stream both");
+        auto fetch = [&](int g) {
+            const int t = t0 + g * kConvGroup;
+            if (t < end) {
+                xin.fetch(g, x + t * P.x_ts, P.x_ts, xs + (long long)t * nblk, nblk, last - t, blk, lane, D);
+                gin.fetch(g, dy + (long long)t * D, D, nullptr, 0, last - t, blk, lane, D);
+            }
+            if constexpr (ASYNC || MIXED) cp_async_commit();
+        };
+        fetch(0);
+        if constexpr (ASYNC) {
 #pragma unroll
-            for (int k = 0; k < kConvBwdAhead; ++k) {
-                xn[k].zero();
-                gn[k].zero();
-                if (tt + k < last) {
-                    xn[k].load(x + (tt + k) * P.x_ts, xs + (long long)(tt + k) * nblk, blk, lane, D);
-                    gn[k].load(dy + (long long)(tt + k) * D, nullptr, blk, lane, D);
+            for (int g = 1; g < kConvRing - 1; ++g) fetch(g);
+        }
+        // one token: its dp, the parameters' sums (SUM), and the gradient W - 1 tokens back
+        auto token = [&](const float (&v)[4], const float (&g)[4], bool sum, float (&o)[4]) {
+            float2 in[2], e[2];
+            pairs(v, in);
+            pairs(g, e);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int j = 0; j < W - 1; ++j) h[j][i] = h[j + 1][i], dp[j][i] = dp[j + 1][i];
+                h[W - 1][i] = in[i];
+                if (P.silu) {
+                    float2 p = bias[i];
+#pragma unroll
+                    for (int j = W - 1; j >= 0; --j) p = __ffma2_rn(w[j][i], h[j][i], p);
+                    const float2 one = make_float2(1.f, 1.f), sg = sigmoid2<PRECISE>(p);
+                    const float2 rest = __ffma2_rn(sg, make_float2(-1.f, -1.f), one);
+                    e[i] = __fmul2_rn(__fmul2_rn(e[i], sg), __ffma2_rn(p, rest, one));
                 }
+                dp[W - 1][i] = e[i];
+                if (sum) {
+                    db[i] = __fadd2_rn(db[i], e[i]);
+#pragma unroll
+                    for (int j = 0; j < W; ++j) dw[j][i] = __ffma2_rn(e[i], h[j][i], dw[j][i]);
+                }
+                float2 d = __fmul2_rn(w[0][i], dp[W - 1][i]);
+#pragma unroll
+                for (int j = 1; j < W; ++j) d = __ffma2_rn(w[j][i], dp[W - 1 - j][i], d);
+                o[2 * i] = d.x, o[2 * i + 1] = d.y;
             }
         };
-        fetch(t0);
-        for (int tt = t0; tt < end; tt += kConvBwdAhead) {
-            Token<T, VEC> xr[kConvBwdAhead];
-            Token<DT, VEC> gr[kConvBwdAhead];
+        for (int g = 0, tt = t0; tt < end; ++g, tt += kConvGroup) {
+            float xv[kConvGroup][4], gv[kConvGroup][4];
+            if constexpr (ASYNC) {
+                if (sizeof(T) == 1) __syncwarp();
+                fetch(g + kConvRing - 1);
+                cp_async_wait<kConvRing - 1>();
+                if (sizeof(T) == 1) __syncwarp();
+            } else if constexpr (MIXED) {
+                cp_async_wait<0>();
+            }
+            xin.get(g, lane, xv);
+            gin.get(g, lane, gv);
+            if constexpr (!ASYNC) fetch(g + 1);
+            const bool states = (first && P.dstate && g == 0) || (P.dstate_out && tt + kConvGroup > P.T - (W - 1));
+            if (!states) {
+                GT *to = dx + ((long long)tt - (W - 1)) * D;
+                if (g > 0 && tt + kConvGroup <= t1) {
 #pragma unroll
-            for (int k = 0; k < kConvBwdAhead; ++k) xr[k] = xn[k], gr[k] = gn[k];
-            if (tt + kConvBwdAhead < end) fetch(tt + kConvBwdAhead);
+                    for (int k = 0; k < kConvGroup; ++k) {
+                        float o[4];
+                        token(xv[k], gv[k], true, o);
+                        row_store<VEC>(to + (long long)k * D, blk, lane, D, o);
+                    }
+                } else {                                    // a run's first and last tokens
 #pragma unroll
-            for (int k = 0; k < kConvBwdAhead; ++k) {
+                    for (int k = 0; k < kConvGroup; ++k) {
+                        float o[4];
+                        token(xv[k], gv[k], tt + k < t1, o);
+                        if (tt + k - (W - 1) >= t0 && tt + k < end) row_store<VEC>(to + (long long)k * D, blk, lane, D, o);
+                    }
+                }
+                continue;
+            }
+#pragma unroll 1
+            for (int k = 0; k < kConvGroup; ++k) {          // where the states' gradients come in
                 const int t = tt + k;
                 if (t >= end) break;
-                float v[4], g[4], o[4];
-                xr[k].get(v);
-                gr[k].get(g);
-                const bool live = t < t1;
+                float o[4], xk[4], gk[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    xk[i] = xv[0][i], gk[i] = gv[0][i];
 #pragma unroll
-                    for (int j = 0; j < W - 1; ++j) h[j][i] = h[j + 1][i], dp[j][i] = dp[j + 1][i];
-                    h[W - 1][i] = v[i];
-                    float e = t < P.T ? g[i] : 0.f;
-                    if (P.silu) {
-                        float p = bias[i];
-#pragma unroll
-                        for (int j = W - 1; j >= 0; --j) p = fmaf(w[j][i], h[j][i], p);
-                        const float sg = sigmoid<PRECISE>(p);
-                        e = t < P.T ? e * sg * fmaf(p, 1.f - sg, 1.f) : 0.f;
-                    }
-                    dp[W - 1][i] = e;
-                    if (live) {
-                        db[i] += e;
-#pragma unroll
-                        for (int j = 0; j < W; ++j) dw[j][i] = fmaf(e, h[j][i], dw[j][i]);
-                    }
-                    float d = 0.f;
-#pragma unroll
-                    for (int j = 0; j < W; ++j) d = fmaf(w[j][i], dp[W - 1 - j][i], d);
-                    o[i] = d;
+                    for (int m = 1; m < kConvGroup; ++m)
+                        if (k == m) xk[i] = xv[m][i], gk[i] = gv[m][i];
                 }
+                token(xk, gk, t < t1, o);
                 const int at = t - (W - 1);         // the token whose gradient is complete
                 const int row = at - (P.T - (W - 1));
                 if (P.dstate_out && row >= 0) {     // it is in state_out as well
@@ -319,8 +491,8 @@ conv_bwd_kernel(const ConvBwd P) {
     for (int i = 0; i < 4; ++i) {
         const int c = lane_channel<VEC>(0, lane, i);
 #pragma unroll
-        for (int j = 0; j < W; ++j) part[warp][j][c] = dw[j][i];
-        part[warp][W][c] = db[i];
+        for (int j = 0; j < W; ++j) part[warp][j][c] = (i & 1) ? dw[j][i / 2].y : dw[j][i / 2].x;
+        part[warp][W][c] = (i & 1) ? db[i / 2].y : db[i / 2].x;
     }
     __syncthreads();
     float *out = P.partial + (b * P.groups + group) * (W + 1) * (long long)D;
@@ -347,10 +519,20 @@ __global__ void conv_params_kernel(int D, int W, const float *__restrict__ sums,
 wkv7_status conv_dims(int B, int T, int D, int W) {
     if (B < 0 || T < 0 || D < 0 || W <= 0) return WKV7_ERR_INVALID_ARG;
     if (W < 2 || W > 4 || D > WKV7_SSM_MAX_D || T > kMaxTokens) return WKV7_ERR_UNSUPPORTED;
-    const long long runs = ((long long)T + kConvRun - 1) / kConvRun + 1;
+    const long long runs = ((long long)T + kConvMinRun - 1) / kConvMinRun + 1;
     // blocks of a launch, and of the step's
     if ((double)B * runs * blocks_of(D) > (double)kMaxGrid) return WKV7_ERR_UNSUPPORTED;
     return WKV7_OK;
+}
+
+// Tokens a run: the fewer, the more a run's start (W - 1 tokens again, the weights)
+// costs, so 64 where that makes 32 warps an SM (8 x 4096 x 2048: 52 us), else 32 or
+// 16 (5 x 2999 x 531 in fp32: 7.4 us at 32, 11.9 at 64).
+int conv_run(int B, int T, int D) {
+    const long long want = 32ll * sm_count();
+    int run = 64;
+    while (run > kConvMinRun && (long long)B * ((T + run - 1) / run) * blocks_of(D) < want) run /= 2;
+    return run;
 }
 
 int conv_groups(int T) {
@@ -365,13 +547,21 @@ template <typename F> void by_width(int W, F &&f) {
     else f(std::integral_constant<int, 4>{});
 }
 
+// a kernel's dynamic shared memory, with leave to use it where it is large
+template <typename K, typename P>
+void conv_launch(K kernel, const P &p, unsigned grid, int threads, size_t smem, cudaStream_t st) {
+    if (smem > 32 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    kernel<<<grid, threads, smem, st>>>(p);
+}
+
 template <typename T, typename ST, typename YT, bool SAVE>
 void launch_conv_fwd(const ConvFwd &P, int W, bool vec, cudaStream_t st) {
     const long long units = (long long)P.B * P.runs * blocks_of(P.D);
     const unsigned grid = (unsigned)((units + kConvWarps - 1) / kConvWarps);
     by_width(W, [&](auto w) {
-        if (vec) conv_fwd_kernel<T, ST, YT, decltype(w)::value, true, SAVE><<<grid, 32 * kConvWarps, 0, st>>>(P);
-        else conv_fwd_kernel<T, ST, YT, decltype(w)::value, false, SAVE><<<grid, 32 * kConvWarps, 0, st>>>(P);
+        constexpr int WW = decltype(w)::value, th = 32 * kConvWarps;
+        if (vec) conv_launch(conv_fwd_kernel<T, ST, YT, WW, true, SAVE>, P, grid, th, kConvWarps * Stream<T, true>::BYTES, st);
+        else conv_launch(conv_fwd_kernel<T, ST, YT, WW, false, SAVE>, P, grid, th, kConvWarps * Stream<T, false>::BYTES, st);
     });
 }
 
@@ -379,8 +569,13 @@ template <typename T, typename ST, typename DT, typename GT>
 void launch_conv_bwd(const ConvBwd &P, int W, bool vec, cudaStream_t st) {
     const unsigned grid = (unsigned)((long long)P.B * P.groups * blocks_of(P.D));
     by_width(W, [&](auto w) {
-        if (vec) conv_bwd_kernel<T, ST, DT, GT, decltype(w)::value, true><<<grid, 32 * kConvBwdWarps, 0, st>>>(P);
-        else conv_bwd_kernel<T, ST, DT, GT, decltype(w)::value, false><<<grid, 32 * kConvBwdWarps, 0, st>>>(P);
+        constexpr int WW = decltype(w)::value, th = 32 * kConvBwdWarps;
+        if (vec)
+            conv_launch(conv_bwd_kernel<T, ST, DT, GT, WW, true>, P, grid, th,
+                        kConvBwdWarps * (Stream<T, true>::BYTES + Stream<DT, true>::BYTES), st);
+        else
+            conv_launch(conv_bwd_kernel<T, ST, DT, GT, WW, false>, P, grid, th,
+                        kConvBwdWarps * (Stream<T, false>::BYTES + Stream<DT, false>::BYTES), st);
     });
 }
 
@@ -412,13 +607,13 @@ wkv7_status wkv7_conv_forward(int B, int T, int D, int W, wkv7_dtype x_dt, wkv7_
         return WKV7_ERR_INVALID_ARG;
     if (T == 0 && !state_out) return WKV7_OK;
     if (q8) x_bs = (long long)T * D, x_ts = D;
-    int runs = (int)(((long long)T + kConvRun - 1) / kConvRun);
-    if (runs == 0) runs = 1;                        // T = 0: the state alone
+    const int run = conv_run(B, T, D), runs = T > 0 ? (T + run - 1) / run : 1;      // T = 0: the state alone
     const ConvFwd P{B, T, D, x, x_bs, x_ts, x_scales, weight, bias, state, lens, silu, y, state_out,
-                    (uint8_t *)codes, scales, runs};
+                    (uint8_t *)codes, scales, runs, run};
     const bool vec = D % 4 == 0 && x_bs % 4 == 0 && x_ts % 4 == 0 && aligned_to(x, 4 * dtype_size(x_dt)) &&
                      aligned_to(y, 4 * dtype_size(y_dt)) && aligned_to(state, 4 * dtype_size(s_dt)) &&
-                     aligned_to(state_out, 4 * dtype_size(s_dt)) && aligned_to(codes, 4);
+                     aligned_to(state_out, 4 * dtype_size(s_dt)) && aligned_to(codes, 4) && aligned_to(weight, 16) &&
+                     aligned_to(bias, 16);
     const bool yf = y_dt == WKV7_F32;
     if (q8) {
         if (yf) launch_conv_fwd<e4m3, float, float, false>(P, W, vec, stream);
@@ -517,7 +712,8 @@ wkv7_status wkv7_conv_backward(int B, int T, int D, int W, wkv7_dtype x_dt, wkv7
                     groups};
     const bool vec = D % 4 == 0 && x_bs % 4 == 0 && x_ts % 4 == 0 && aligned_to(x, 4 * dtype_size(x_dt)) &&
                      aligned_to(dy, 4 * dtype_size(dy_dt)) && aligned_to(dx, 4 * dtype_size(g_dt)) &&
-                     aligned_to(state, 4 * dtype_size(s_dt)) && aligned_to(dstate, 16) && aligned_to(dstate_out, 16);
+                     aligned_to(state, 4 * dtype_size(s_dt)) && aligned_to(dstate, 16) && aligned_to(dstate_out, 16) &&
+                     aligned_to(weight, 16) && aligned_to(bias, 16);
     const bool df = dy_dt == WKV7_F32, gf = g_dt == WKV7_F32;
 #define WKV7_BWD(T, ST, DT, GT) launch_conv_bwd<T, ST, DT, GT>(P, W, vec, stream)
     if (q8) {

@@ -104,7 +104,7 @@ template <int BYTES> __device__ __forceinline__ void copy_async(void *dst, const
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
-    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 __device__ __forceinline__ float rcp(float x) {
@@ -116,6 +116,12 @@ __device__ __forceinline__ float rcp(float x) {
 // result's half step for every |x| < 88; PRECISE (fp32 results) uses expf.
 template <bool PRECISE> __device__ __forceinline__ float sigmoid(float x) {
     return rcp(1.f + (PRECISE ? expf(-x) : ex2(-x * kLog2e)));
+}
+template <bool PRECISE> __device__ __forceinline__ float2 sigmoid2(float2 x) {
+    if constexpr (PRECISE) return make_float2(sigmoid<true>(x.x), sigmoid<true>(x.y));
+    const float2 t = __fmul2_rn(x, make_float2(-kLog2e, -kLog2e));
+    const float2 d = __fadd2_rn(make_float2(ex2(t.x), ex2(t.y)), make_float2(1.f, 1.f));
+    return make_float2(rcp(d.x), rcp(d.y));
 }
 // log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in (0, 1]; log1p(e) / e by its
 // Chebyshev interpolant of degree 9 on [0, 1] (off by 6e-9 of the value, 1e-7
@@ -168,11 +174,12 @@ __device__ __forceinline__ float to_odd(float s, float err) {
     const bool moves = (err < 0.f || err > 0.f) && !(b & 1);
     return moves ? __int_as_float(b + (((err > 0.f) == (b >= 0)) ? 1 : -1)) : s;
 }
-// (a + b) - fl(a + b), exactly: the two-sum of Knuth (The Art of Computer
-// Programming, vol. 2, section 4.2.2); s = fl(a + b)
-__device__ __forceinline__ float sum_error(float a, float b, float s) {
-    const float t = s - a;
-    return (a - (s - t)) + (b - t);
+// (a + b) - fl(a + b), exactly, of two pairs: the two-sum of Knuth (The Art of
+// Computer Programming, vol. 2, section 4.2.2); s = fl(a + b)
+__device__ __forceinline__ float2 sub2(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.f, -1.f), a); }
+__device__ __forceinline__ float2 sum_error(float2 a, float2 b, float2 s) {
+    const float2 t = sub2(s, a);
+    return __fadd2_rn(sub2(a, sub2(s, t)), sub2(b, t));
 }
 
 // ---- the 8-bit format --------------------------------------------------------------
@@ -185,11 +192,12 @@ __device__ __forceinline__ uint32_t act8_exponent(uint32_t b) {     // b: amax's
 }
 
 // The warp's block of 128 values, 4 in each lane.  Bits of absolute values order
-// like the values, so amax is one warp-wide integer maximum.
+// like the values, so amax is one warp-wide integer maximum.  NaN drops out of it
+// (and converts to the NaN code by itself); an infinity shows.
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t act8_top(const float (&v)[4]) {
-    const uint32_t m = max(max(abs_bits(v[0]), abs_bits(v[1])), max(abs_bits(v[2]), abs_bits(v[3])));
-    return __reduce_max_sync(0xffffffffu, m);
+    const float m = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+    return __reduce_max_sync(0xffffffffu, m == m ? __float_as_uint(m) : 0u);
 }
 __device__ __forceinline__ uint32_t act8_pack(const float (&q)[4]) {
     const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(q[0], q[1]), __NV_SATFINITE, __NV_E4M3);
@@ -221,25 +229,48 @@ __device__ __forceinline__ float act8_encode(const float (&x)[4], uint32_t &code
     codes = act8_pack(v);
     return __uint_as_float(e << 23);
 }
-// The same where every value is known to within 2^-21 of itself only: false if a
-// code or the scale could depend on more (a scaled value next to the middle
-// between two codes or among the codes' subnormals, amax next to a power's
-// border, numbers too large).  Uniform in the warp.
+// K blocks one after another; the usual case without a branch between them, so that their maxima overlap
+template <int K>
+__device__ __forceinline__ void act8_encode_all(const float (&x)[K][4], uint32_t (&codes)[K], float (&scale)[K]) {
+    uint32_t top[K], worst = 0;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        top[k] = act8_top(x[k]);
+        worst = max(worst, top[k]);
+    }
+    if (worst >= 0x7f600000u) {                 // infinities, NaN, or within a step of 2^128
+#pragma unroll
+        for (int k = 0; k < K; ++k) scale[k] = act8_encode(x[k], codes[k]);
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const uint32_t e = act8_exponent(top[k]);
+        const float inv = __uint_as_float((254u - e) << 23);
+        const float q[4] = {x[k][0] * inv, x[k][1] * inv, x[k][2] * inv, x[k][3] * inv};
+        codes[k] = act8_pack(q);
+        scale[k] = __uint_as_float(e << 23);
+    }
+}
+// The same where every value is known to within 2^-22 of itself only: false if a
+// code or the scale could depend on more, that is if the values a 2^-21 below and
+// above have other codes, amax is next to a power's border, or numbers are too
+// large or too small for the scale.  Uniform in the warp.
 __device__ __forceinline__ bool act8_encode_sure(const float (&x)[4], uint32_t &codes, float &scale) {
     const uint32_t top = act8_top(x), e = act8_exponent(top);
     const float inv = __uint_as_float((254u - e) << 23);
-    bool close = (top & 0x7fffffu) - 0x5ffff8u <= 16u || top > 0x7b000000u || top < 0x08000000u;
-    float q[4];
+    const bool border = (top & 0x7fffffu) - 0x5ffff8u <= 16u || top > 0x7b000000u || top < 0x08000000u;
+    float lo[4], hi[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        q[i] = x[i] * inv;
-        const uint32_t b = __float_as_uint(q[i]);
-        // the middle between two codes: the leading bit behind the three that are kept, alone
-        close |= (b & 0xfffffu) - 0x7fff8u <= 16u || (fabsf(q[i]) < 0.015625f && q[i] != 0.f);
+    for (int i = 0; i < 4; i += 2) {
+        const float2 q = make_float2(x[i], x[i + 1]);
+        const float a = inv * (1.f - 0x1p-21f), b = inv * (1.f + 0x1p-21f);
+        const float2 l = __fmul2_rn(q, make_float2(a, a)), h = __fmul2_rn(q, make_float2(b, b));
+        lo[i] = l.x, lo[i + 1] = l.y, hi[i] = h.x, hi[i + 1] = h.y;
     }
-    codes = act8_pack(q);
+    codes = act8_pack(lo);
     scale = __uint_as_float(e << 23);
-    return !__any_sync(0xffffffffu, close);
+    return !__any_sync(0xffffffffu, border || codes != act8_pack(hi));
 }
 
 // ---- rows cut into blocks of 128 channels, a warp to a block -------------------------

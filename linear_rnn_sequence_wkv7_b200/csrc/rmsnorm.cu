@@ -14,13 +14,15 @@
 // is therefore carried in fp64 from every four elements on, and where a block has
 // a y next to a border (one block in a thousand) y is taken in two floats (value
 // and error) and rounded once.
+#include <type_traits>
+
 #include "mixer.cuh"
 
 namespace wkv7 {
 namespace mixer {
 namespace {
 
-constexpr int kNormMaxWarps = 32;
+constexpr int kNormMaxWarps = 16;
 
 // E: whether 8-bit codes can be among the types; WIDE: whether fp32 can
 template <bool WIDE, bool E, typename F> __device__ __forceinline__ void by_dtype(wkv7_dtype dt, F &&f) {
@@ -30,19 +32,19 @@ template <bool WIDE, bool E, typename F> __device__ __forceinline__ void by_dtyp
 }
 // MB blocks of a row, one branch around the batch
 template <bool VEC, int MB, bool WIDE, bool E>
-__device__ __forceinline__ void batch_load(const void *p, wkv7_dtype dt, long long off, int blk0, int step, int lane,
-                                           int D, float (&f)[MB][4]) {
+__device__ __forceinline__ void batch_load(const void *p, wkv7_dtype dt, int blk0, int step, int lane, int D,
+                                           float (&f)[MB][4]) {
     by_dtype<WIDE, E>(dt, [&](auto t) {
-        const decltype(t) *row = static_cast<const decltype(t) *>(p) + off;
+        const decltype(t) *row = static_cast<const decltype(t) *>(p);
 #pragma unroll
         for (int m = 0; m < MB; ++m) row_load<VEC>(row, blk0 + m * step, lane, D, f[m]);
     });
 }
 
-// Rows on their way: kAhead rows of each tensor, copied to shared memory
+// Rows on their way or in use: kAhead rows of each tensor, copied to shared memory
 // (cp.async) by the thread that reads them, so no barrier is needed.  A slot is
 // four values, 8 bytes or (WIDE) 16; slots behind the row's end stay zero.
-constexpr int kAhead = 4;
+constexpr int kAhead = 3;
 template <int MB, bool WIDE, int TENSORS> struct Ring {
     static constexpr int SLOT = WIDE ? 16 : 8;
     unsigned char *base;
@@ -54,10 +56,10 @@ template <int MB, bool WIDE, int TENSORS> struct Ring {
             for (int k = 0; k < SLOT; k += 8) *reinterpret_cast<uint2 *>(slot(0, 0, i) + k) = make_uint2(0, 0);
     }
     template <bool E>
-    __device__ __forceinline__ void fetch(int stage, int tensor, const void *p, wkv7_dtype dt, long long off, int blk0,
-                                          int step, int lane, int D) const {
+    __device__ __forceinline__ void fetch(int stage, int tensor, const void *p, wkv7_dtype dt, int blk0, int step, int lane,
+                                          int D) const {
         by_dtype<WIDE, E>(dt, [&](auto t) {
-            const decltype(t) *row = static_cast<const decltype(t) *>(p) + off;
+            const decltype(t) *row = static_cast<const decltype(t) *>(p);
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
                 const int c = lane_channel<true>(blk0 + m * step, lane, 0);
@@ -66,43 +68,52 @@ template <int MB, bool WIDE, int TENSORS> struct Ring {
         });
     }
     template <bool E>
-    __device__ __forceinline__ void get(int stage, int tensor, wkv7_dtype dt, float (&f)[MB][4]) const {
+    __device__ __forceinline__ void get(int stage, int tensor, int m, wkv7_dtype dt, float (&f)[4]) const {
         by_dtype<WIDE, E>(dt, [&](auto t) {
-#pragma unroll
-            for (int m = 0; m < MB; ++m) {
-                Vec<decltype(t), 4> v;
-                const uint32_t *w = reinterpret_cast<const uint32_t *>(slot(stage, tensor, m));
-                if constexpr (sizeof(v.w) == 16) {
-                    const uint4 q = *reinterpret_cast<const uint4 *>(w);
-                    v.w[0] = q.x, v.w[1] = q.y, v.w[2] = q.z, v.w[3] = q.w;
-                } else if constexpr (sizeof(v.w) == 8) {
-                    const uint2 q = *reinterpret_cast<const uint2 *>(w);
-                    v.w[0] = q.x, v.w[1] = q.y;
-                } else {
-                    v.w[0] = w[0];
-                }
-                v.get(f[m]);
+            Vec<decltype(t), 4> v;
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(slot(stage, tensor, m));
+            if constexpr (sizeof(v.w) == 16) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(w);
+                v.w[0] = q.x, v.w[1] = q.y, v.w[2] = q.z, v.w[3] = q.w;
+            } else if constexpr (sizeof(v.w) == 8) {
+                const uint2 q = *reinterpret_cast<const uint2 *>(w);
+                v.w[0] = q.x, v.w[1] = q.y;
+            } else {
+                v.w[0] = w[0];
             }
+            v.get(f);
         });
+    }
+    template <bool E>
+    __device__ __forceinline__ void get(int stage, int tensor, wkv7_dtype dt, float (&f)[MB][4]) const {
+#pragma unroll
+        for (int m = 0; m < MB; ++m) get<E>(stage, tensor, m, dt, f[m]);
     }
 };
 template <int MB, bool WIDE> constexpr size_t ring_bytes(int tensors, int threads) {
     return (size_t)kAhead * tensors * MB * threads * (WIDE ? 16 : 8);
 }
 
-template <bool VEC, int MB>
-__device__ __forceinline__ void batch_store(void *p, wkv7_dtype dt, long long off, int blk0, int step, int lane,
-                                            int D, const float (&f)[MB][4]) {
-    if (dt == WKV7_BF16) {
-        bf16 *row = static_cast<bf16 *>(p) + off;
+template <bool VEC, int MB, bool WIDE>
+__device__ __forceinline__ void batch_store(void *p, wkv7_dtype dt, int blk0, int step, int lane, int D,
+                                            const float (&f)[MB][4]) {
+    if (!WIDE || dt == WKV7_BF16) {
 #pragma unroll
-        for (int m = 0; m < MB; ++m) row_store<VEC>(row, blk0 + m * step, lane, D, f[m]);
+        for (int m = 0; m < MB; ++m) row_store<VEC>(static_cast<bf16 *>(p), blk0 + m * step, lane, D, f[m]);
     } else {
-        float *row = static_cast<float *>(p) + off;
 #pragma unroll
-        for (int m = 0; m < MB; ++m) row_store<VEC>(row, blk0 + m * step, lane, D, f[m]);
+        for (int m = 0; m < MB; ++m) row_store<VEC>(static_cast<float *>(p), blk0 + m * step, lane, D, f[m]);
     }
 }
+__device__ __forceinline__ long long elem_size(wkv7_dtype dt) { return dt == WKV7_F32 ? 4 : dt == WKV7_BF16 ? 2 : 1; }
+// A tensor's rows as a block walks them
+struct Rows {
+    char *p;
+    long long step;
+    __device__ __forceinline__ Rows(const void *base, wkv7_dtype dt, long long ld)
+        : p(base ? (char *)base + blockIdx.x * ld * elem_size(dt) : nullptr), step(gridDim.x * ld * elem_size(dt)) {}
+    __device__ __forceinline__ void next() { p += step; }
+};
 
 // sum over the block's warps of one value a warp; every thread gets it
 template <typename F> __device__ __forceinline__ F block_add(F x, F *shared, int warp, int warps) {
@@ -116,7 +127,9 @@ template <typename F> __device__ __forceinline__ F block_add(F x, F *shared, int
 }
 
 // blocks of 128 a warp holds, and the threads of a row's block at most
-__host__ __device__ constexpr int norm_max_threads(int MB) { return MB == 1 ? 256 : MB == 2 ? 512 : 1024; }
+__host__ __device__ constexpr int norm_max_threads(int MB) { return MB == 1 ? 64 : MB == 2 ? 128 : MB == 4 ? 256 : 512; }
+// and the threads on an SM that the registers leave room for
+__host__ __device__ constexpr int norm_sm_threads(int MB) { return MB <= 2 ? 1024 : 512; }
 
 struct NormFwd {
     long long rows;
@@ -133,87 +146,136 @@ struct NormFwd {
     float *s_scales, *rstd;
 };
 
-// A block takes rows blockIdx.x, + gridDim.x, ...  MB <= 2 with vector accesses:
-// the next rows are on their way and the weight stays in registers.
-template <bool VEC, int MB, bool WIDE>
-__global__ void __launch_bounds__(norm_max_threads(MB), 1024 / norm_max_threads(MB))
+// A block takes rows blockIdx.x, + gridDim.x, ...  RING: the next rows are on their
+// way.  WIDE: fp32 can be among the types.
+template <bool VEC, int MB, bool WIDE, bool RING>
+__global__ void __launch_bounds__(norm_max_threads(MB), norm_sm_threads(MB) / norm_max_threads(MB))
 rmsnorm_fwd_kernel(const NormFwd P) {
-    constexpr bool RING = VEC && MB <= 2, KEEP = MB <= 2;
+    constexpr bool KEEP = MB <= 4;      // the weight stays in registers
     __shared__ double shared[2][kNormMaxWarps];
     extern __shared__ __align__(16) unsigned char ring_mem[];
     const Ring<MB, WIDE, 2> ring{ring_mem};
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int nblk = (P.D + kBlk - 1) / kBlk, D = P.D;
     float w[MB][4];
-    auto fetch = [&](long long row, int stage) {
-        if (row < P.rows) {
-            ring.template fetch<false>(stage, 0, P.x, P.x_dt, row * P.x_ld, warp, warps, lane, D);
-            if (P.residual) ring.template fetch<false>(stage, 1, P.residual, P.r_dt, row * D, warp, warps, lane, D);
+    Rows x(P.x, P.x_dt, P.x_ld), res(P.residual, P.r_dt, D), res_out(P.residual_out, P.r_dt, D), y(P.y, P.y_dt, D);
+    Rows codes(P.s_codes, WKV7_E4M3, D), scales(P.s_scales, WKV7_F32, nblk), y_scales(P.y_scales, WKV7_F32, nblk);
+    long long ahead = blockIdx.x;       // the row that is fetched next
+    auto fetch = [&](int stage) {
+        if (ahead < P.rows) {
+            ring.template fetch<false>(stage, 0, x.p, P.x_dt, warp, warps, lane, D);
+            x.next();
+            if (P.residual) {
+                ring.template fetch<false>(stage, 1, res.p, P.r_dt, warp, warps, lane, D);
+                res.next();
+            }
+            ahead += gridDim.x;
         }
         cp_async_commit();
     };
     if constexpr (RING) {
         ring.clear();
 #pragma unroll
-        for (int i = 0; i < kAhead - 1; ++i) fetch(blockIdx.x + (long long)i * gridDim.x, i);
+        for (int i = 0; i < kAhead - 1; ++i) fetch(i);
     }
     if (KEEP) {
 #pragma unroll
         for (int m = 0; m < MB; ++m) row_load<VEC>(P.weight, warp + m * warps, lane, D, w[m]);
     }
     int turn = 0, stage = 0;
-    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x, turn ^= 1, stage = (stage + 1) % kAhead) {
-        float s[MB][4], o[MB][4];   // the sum to nearest, and rounded to odd for what keeps fewer bits
+    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x) {
+        // No branch inside the loops over m: the blocks' work overlaps
+        float s[MB][4];
+        const int now = stage;
         if constexpr (RING) {
-            fetch(row + (kAhead - 1ll) * gridDim.x, (stage + kAhead - 1) % kAhead);
+            fetch(stage == 0 ? kAhead - 1 : stage - 1);
             cp_async_wait<kAhead - 1>();
-            ring.template get<false>(stage, 0, P.x_dt, s);
-            if (P.residual) ring.template get<false>(stage, 1, P.r_dt, o);
-        } else {
-            batch_load<VEC, MB, WIDE, false>(P.x, P.x_dt, row * P.x_ld, warp, warps, lane, D, s);
-            if (P.residual) batch_load<VEC, MB, WIDE, false>(P.residual, P.r_dt, row * D, warp, warps, lane, D, o);
+            stage = stage == kAhead - 1 ? 0 : stage + 1;
+        }
+        auto get_x = [&](float (&f)[MB][4]) {
+            if constexpr (RING) ring.template get<false>(now, 0, P.x_dt, f);
+            else batch_load<VEC, MB, WIDE, false>(x.p, P.x_dt, warp, warps, lane, D, f);
+        };
+        auto get_res = [&](float (&f)[MB][4]) {
+            if constexpr (RING) ring.template get<false>(now, 1, P.r_dt, f);
+            else batch_load<VEC, MB, WIDE, false>(res.p, P.r_dt, warp, warps, lane, D, f);
+        };
+        auto error = [&](const float (&a)[4], const float (&b)[4], const float (&t)[4], float (&e)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+                const float2 v = sum_error(make_float2(a[i], a[i + 1]), make_float2(b[i], b[i + 1]),
+                                           make_float2(t[i], t[i + 1]));
+                e[i] = v.x, e[i + 1] = v.y;
+            }
+        };
+        bool inexact = false;       // a sum of two bf16 numbers only where they are 2^16 apart
+        get_x(s);
+        if (P.residual) {
+            float r[MB][4];
+            uint32_t bits = 0;
+            get_res(r);
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                float t[4], e[4];
+#pragma unroll
+                for (int i = 0; i < 4; i += 2) {
+                    const float2 v = __fadd2_rn(make_float2(s[m][i], s[m][i + 1]), make_float2(r[m][i], r[m][i + 1]));
+                    t[i] = v.x, t[i + 1] = v.y;
+                }
+                error(s[m], r[m], t, e);
+                bits |= abs_bits(e[0]) | abs_bits(e[1]) | abs_bits(e[2]) | abs_bits(e[3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[m][i] = t[i];
+            }
+            inexact = __any_sync(0xffffffffu, bits != 0);
         }
         double sum = 0;
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
-            if (P.residual) {
-                float err[4];
-                bool exact = true;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = s[m][i], b = o[m][i];
-                    s[m][i] = a + b;
-                    err[i] = sum_error(a, b, s[m][i]);
-                    exact &= err[i] == 0.f;
-                    o[m][i] = s[m][i];
-                }
-                if (!exact) {           // of two bf16 numbers: only where they are 2^16 apart
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[m][i] = to_odd(s[m][i], err[i]);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[m][i] = s[m][i];
+            const float2 lo = make_float2(s[m][0], s[m][1]), hi = make_float2(s[m][2], s[m][3]);
+            const float2 sq = __ffma2_rn(hi, hi, __fmul2_rn(lo, lo));
+            sum += (double)(sq.x + sq.y);
+        }
+        auto keep = [&](const float (&o)[MB][4]) {      // what keeps fewer bits of the sum
+            if (P.residual_out) {
+                if (!WIDE || P.r_dt == WKV7_BF16) batch_store<VEC, MB, false>(res_out.p, WKV7_BF16, warp, warps, lane, D, o);
+                else batch_store<VEC, MB, true>(res_out.p, WKV7_F32, warp, warps, lane, D, s);
             }
-            sum += (double)fmaf(s[m][0], s[m][0], fmaf(s[m][1], s[m][1], fmaf(s[m][2], s[m][2], s[m][3] * s[m][3])));
-        }
-        if (P.residual_out) {
-            if (P.r_dt == WKV7_BF16) batch_store<VEC, MB>(P.residual_out, WKV7_BF16, row * D, warp, warps, lane, D, o);
-            else batch_store<VEC, MB>(P.residual_out, WKV7_F32, row * D, warp, warps, lane, D, s);
-        }
-        if (P.s_codes) {
+            if (P.s_codes) {
+                uint32_t q[MB];
+                float scale[MB];
+                act8_encode_all(o, q, scale);
+#pragma unroll
+                for (int m = 0; m < MB; ++m) {
+                    const int blk = warp + m * warps;
+                    row_store_codes<VEC>(reinterpret_cast<uint8_t *>(codes.p), blk, lane, D, q[m]);
+                    if (lane == 0 && blk < nblk) reinterpret_cast<float *>(scales.p)[blk] = scale[m];
+                }
+            }
+        };
+        if (!inexact) keep(s);
+        else {                      // rounded to odd, it rounds to fewer bits as the exact sum does
+            float o[MB][4], r[MB][4];
+            get_x(o);
+            get_res(r);
 #pragma unroll
             for (int m = 0; m < MB; ++m) {
-                const int blk = warp + m * warps;
-                if (blk >= nblk) break;
-                uint32_t q;
-                const float scale = act8_encode(o[m], q);
-                row_store_codes<VEC>(P.s_codes + row * D, blk, lane, D, q);
-                if (lane == 0) P.s_scales[row * nblk + blk] = scale;
+                float e[4];
+                error(o[m], r[m], s[m], e);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[m][i] = to_odd(s[m][i], e[i]);
             }
+            keep(o);
         }
+        if constexpr (!RING) {
+            x.next();
+            res.next();
+        }
+        res_out.next();
+        codes.next(), scales.next();
         // two buffers in turn: a warp that is a row ahead does not overwrite sums still being read
         sum = block_add(sum, shared[turn], warp, warps);
+        turn ^= 1;
         // 1 / sqrt in fp32, and one Newton step in fp64
         const double mean = fma(sum, P.inv_D, P.eps), r0 = (double)rsqrtf((float)mean);
         const double inv = isinf(r0) ? r0 : fma(0.5 * r0, fma(-mean * r0, r0, 1.0), r0);
@@ -228,30 +290,47 @@ rmsnorm_fwd_kernel(const NormFwd P) {
             for (int m = 0; m < MB; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[m][i] = s[m][i] * ih * w[m][i];
-            batch_store<VEC, MB>(P.y, P.y_dt, row * D, warp, warps, lane, D, s);
+            batch_store<VEC, MB, true>(y.p, P.y_dt, warp, warps, lane, D, s);
+            y.next();
             continue;
+        }
+        uint32_t q[MB];
+        float scale[MB];
+        bool sure[MB], all = true;
+#pragma unroll
+        for (int m = 0; m < MB; ++m) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {        // off by 3 half steps at most
+                const float2 t = __fmul2_rn(make_float2(s[m][i], s[m][i + 1]), make_float2(w[m][i], w[m][i + 1]));
+                const float2 u = __fmul2_rn(t, make_float2(ih, ih));
+                v[i] = u.x, v[i + 1] = u.y;
+            }
+            sure[m] = act8_encode_sure(v, q[m], scale[m]);
+            all &= sure[m];
+        }
+        if (!all) {
+#pragma unroll
+            for (int m = 0; m < MB; ++m) {
+                if (sure[m]) continue;
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float p = s[m][i] * w[m][i], pl = fmaf(s[m][i], w[m][i], -p);
+                    const float t = p * ih, tl = fmaf(p, ih, -t) + fmaf(pl, ih, p * il);
+                    const float top = t + tl;
+                    v[i] = to_odd(top, tl - (top - t));
+                }
+                scale[m] = act8_encode(v, q[m]);
+            }
         }
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             const int blk = warp + m * warps;
-            if (blk >= nblk) break;
-            float v[4], scale;
-            uint32_t q;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = s[m][i] * w[m][i] * ih;      // off by 3 half steps at most
-            if (!act8_encode_sure(v, q, scale)) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float p = s[m][i] * w[m][i], pl = fmaf(s[m][i], w[m][i], -p);
-                    const float y = p * ih, yl = fmaf(p, ih, -y) + fmaf(pl, ih, p * il);
-                    const float top = y + yl;
-                    v[i] = to_odd(top, yl - (top - y));
-                }
-                scale = act8_encode(v, q);
-            }
-            row_store_codes<VEC>(static_cast<uint8_t *>(P.y) + row * D, blk, lane, D, q);
-            if (lane == 0) P.y_scales[row * nblk + blk] = scale;
+            row_store_codes<VEC>(reinterpret_cast<uint8_t *>(y.p), blk, lane, D, q[m]);
+            if (lane == 0 && blk < nblk) reinterpret_cast<float *>(y_scales.p)[blk] = scale[m];
         }
+        y.next(), y_scales.next();
     }
 }
 
@@ -269,10 +348,11 @@ struct NormBwd {
 
 // The same walk over rows; a block's share of dw goes to partial[blockIdx.x].
 // KEEP: w and dw stay in registers (dw in shared memory otherwise).
-template <bool VEC, int MB, bool WIDE>
-__global__ void __launch_bounds__(norm_max_threads(MB), 1024 / norm_max_threads(MB))
+template <bool VEC, int MB, bool WIDE, bool RING>
+__global__ void __launch_bounds__(norm_max_threads(MB), norm_sm_threads(MB) / norm_max_threads(MB))
 rmsnorm_bwd_kernel(const NormBwd P) {
-    constexpr bool RING = VEC && MB <= 2, KEEP = MB <= 2;
+    constexpr bool KEEP = MB <= 4;
+    static_assert(KEEP || !RING, "dw and the rows share the dynamic shared memory");
     __shared__ float shared[2][kNormMaxWarps];
     extern __shared__ __align__(16) unsigned char ring_mem[];
     const Ring<MB, WIDE, 3> ring{ring_mem};
@@ -281,29 +361,44 @@ rmsnorm_bwd_kernel(const NormBwd P) {
     const int nblk = (P.D + kBlk - 1) / kBlk, D = P.D;
     float w[MB][4], dw[MB][4];
     float next_r = 0.f, next_scale[MB];
-    auto fetch = [&](long long row, int stage) {
-        if (row < P.rows) {
-            ring.template fetch<true>(stage, 0, P.s, P.s_dt, row * D, warp, warps, lane, D);
-            ring.template fetch<false>(stage, 1, P.dy, P.dy_dt, row * D, warp, warps, lane, D);
-            if (P.dres) ring.template fetch<false>(stage, 2, P.dres, P.g_dt, row * D, warp, warps, lane, D);
+    Rows sr(P.s, P.s_dt, D), gr(P.dy, P.dy_dt, D), dr(P.dres, P.g_dt, D), xr(P.dx, P.g_dt, D);
+    Rows qr(P.s_scales, WKV7_F32, nblk), rr(P.rstd, WKV7_F32, 1);
+    long long ahead = blockIdx.x, small = blockIdx.x;       // the rows that are fetched next
+    auto fetch = [&](int stage) {
+        if (ahead < P.rows) {
+            ring.template fetch<true>(stage, 0, sr.p, P.s_dt, warp, warps, lane, D);
+            ring.template fetch<false>(stage, 1, gr.p, P.dy_dt, warp, warps, lane, D);
+            sr.next(), gr.next();
+            if (P.dres) {
+                ring.template fetch<false>(stage, 2, dr.p, P.g_dt, warp, warps, lane, D);
+                dr.next();
+            }
+            ahead += gridDim.x;
         }
         cp_async_commit();
     };
-    auto fetch_small = [&](long long row) {
-        if (row >= P.rows) return;
-        next_r = __ldg(P.rstd + row);
+    auto fetch_small = [&]() {
+        if (small >= P.rows) return;
+        small += gridDim.x;
+        next_r = __ldg(reinterpret_cast<const float *>(rr.p));
+        rr.next();
+        if (P.s_dt == WKV7_E4M3) {
 #pragma unroll
-        for (int m = 0; m < MB; ++m) {
-            const int blk = warp + m * warps;
-            next_scale[m] = (P.s_dt == WKV7_E4M3 && blk < nblk) ? __ldg(P.s_scales + row * nblk + blk) : 1.f;
+            for (int m = 0; m < MB; ++m) {
+                const int blk = warp + m * warps;
+                next_scale[m] = blk < nblk ? __ldg(reinterpret_cast<const float *>(qr.p) + blk) : 0.f;
+            }
+            qr.next();
         }
     };
     if constexpr (RING) {
         ring.clear();
 #pragma unroll
-        for (int i = 0; i < kAhead - 1; ++i) fetch(blockIdx.x + (long long)i * gridDim.x, i);
+        for (int i = 0; i < kAhead - 1; ++i) fetch(i);
     }
-    fetch_small(blockIdx.x);
+#pragma unroll
+    for (int m = 0; m < MB; ++m) next_scale[m] = 1.f;
+    fetch_small();
 #pragma unroll
     for (int m = 0; m < MB; ++m) {
         if (KEEP) row_load<VEC>(P.weight, warp + m * warps, lane, D, w[m]);
@@ -314,48 +409,69 @@ rmsnorm_bwd_kernel(const NormBwd P) {
         }
     }
     int turn = 0, stage = 0;
-    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x, turn ^= 1, stage = (stage + 1) % kAhead) {
+    for (long long row = blockIdx.x; row < P.rows; row += gridDim.x) {
         float s[MB][4], g[MB][4];
+        const int now = stage;
         if constexpr (RING) {
-            fetch(row + (kAhead - 1ll) * gridDim.x, (stage + kAhead - 1) % kAhead);
+            fetch(stage == 0 ? kAhead - 1 : stage - 1);
             cp_async_wait<kAhead - 1>();
-            ring.template get<true>(stage, 0, P.s_dt, s);
-            ring.template get<false>(stage, 1, P.dy_dt, g);
+            ring.template get<true>(now, 0, P.s_dt, s);
+            ring.template get<false>(now, 1, P.dy_dt, g);
+            stage = stage == kAhead - 1 ? 0 : stage + 1;
         } else {
-            batch_load<VEC, MB, WIDE, true>(P.s, P.s_dt, row * D, warp, warps, lane, D, s);
-            batch_load<VEC, MB, WIDE, false>(P.dy, P.dy_dt, row * D, warp, warps, lane, D, g);
+            batch_load<VEC, MB, WIDE, true>(sr.p, P.s_dt, warp, warps, lane, D, s);
+            batch_load<VEC, MB, WIDE, false>(gr.p, P.dy_dt, warp, warps, lane, D, g);
+            sr.next(), gr.next();
         }
         const float r = next_r;
-        float c = 0.f;
+        float2 c2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int m = 0; m < MB; ++m) {
             const float q = next_scale[m] * r;
             if (!KEEP) row_load<VEC>(P.weight, warp + m * warps, lane, D, w[m]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float xh = s[m][i] * q;
-                if (KEEP) dw[m][i] = fmaf(g[m][i], xh, dw[m][i]);
-                else s_dw[(4 * m + i) * blockDim.x + threadIdx.x] += g[m][i] * xh;
-                s[m][i] = xh;
-                g[m][i] *= w[m][i];
-                c = fmaf(g[m][i], xh, c);
+            for (int i = 0; i < 4; i += 2) {
+                const float2 xh = __fmul2_rn(make_float2(s[m][i], s[m][i + 1]), make_float2(q, q));
+                const float2 gg = make_float2(g[m][i], g[m][i + 1]);
+                if (KEEP) {
+                    const float2 a = __ffma2_rn(gg, xh, make_float2(dw[m][i], dw[m][i + 1]));
+                    dw[m][i] = a.x, dw[m][i + 1] = a.y;
+                } else {
+                    s_dw[(4 * m + i) * blockDim.x + threadIdx.x] += gg.x * xh.x;
+                    s_dw[(4 * m + i + 1) * blockDim.x + threadIdx.x] += gg.y * xh.y;
+                }
+                const float2 wg = __fmul2_rn(gg, make_float2(w[m][i], w[m][i + 1]));
+                c2 = __ffma2_rn(wg, xh, c2);
+                s[m][i] = xh.x, s[m][i + 1] = xh.y;
+                g[m][i] = wg.x, g[m][i + 1] = wg.y;
             }
         }
-        fetch_small(row + gridDim.x);
-        c = block_add(c, shared[turn], warp, warps) * P.inv_D;
+        fetch_small();
+        // two buffers in turn, as in the forward
+        const float c = block_add(c2.x + c2.y, shared[turn], warp, warps) * P.inv_D;
+        turn ^= 1;
+        const float2 nc = make_float2(-c, -c), r2 = make_float2(r, r);
 #pragma unroll
         for (int m = 0; m < MB; ++m)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[m][i] = r * fmaf(-c, s[m][i], g[m][i]);
+            for (int i = 0; i < 4; i += 2) {
+                const float2 v = __fmul2_rn(r2, __ffma2_rn(nc, make_float2(s[m][i], s[m][i + 1]),
+                                                           make_float2(g[m][i], g[m][i + 1])));
+                s[m][i] = v.x, s[m][i + 1] = v.y;
+            }
         if (P.dres) {
-            if constexpr (RING) ring.template get<false>(stage, 2, P.g_dt, g);
-            else batch_load<VEC, MB, WIDE, false>(P.dres, P.g_dt, row * D, warp, warps, lane, D, g);
+            if constexpr (RING) ring.template get<false>(now, 2, P.g_dt, g);
+            else {
+                batch_load<VEC, MB, WIDE, false>(dr.p, P.g_dt, warp, warps, lane, D, g);
+                dr.next();
+            }
 #pragma unroll
             for (int m = 0; m < MB; ++m)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) s[m][i] += g[m][i];
         }
-        batch_store<VEC, MB>(P.dx, P.g_dt, row * D, warp, warps, lane, D, s);
+        batch_store<VEC, MB, true>(xr.p, P.g_dt, warp, warps, lane, D, s);
+        xr.next();
     }
     if (!KEEP) {
 #pragma unroll
@@ -363,21 +479,22 @@ rmsnorm_bwd_kernel(const NormBwd P) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) dw[m][i] = s_dw[(4 * m + i) * blockDim.x + threadIdx.x];
     }
-    batch_store<VEC, MB>(P.partial, WKV7_F32, (long long)blockIdx.x * D, warp, warps, lane, D, dw);
+    batch_store<VEC, MB, true>(P.partial + (size_t)blockIdx.x * D, WKV7_F32, warp, warps, lane, D, dw);
 }
 
-int norm_batch(int nblk) { return nblk <= 8 ? 1 : nblk <= 32 ? 2 : 4; }
+// A row's fixed work (the sum over warps, the root) costs a warp some 150
+// instructions, so a warp takes four blocks where the row has them.
+int norm_batch(int nblk) { return nblk <= 2 ? 1 : nblk <= 8 ? 2 : nblk <= 32 ? 4 : 8; }
 
 int norm_threads(int nblk) { return 32 * ((nblk + norm_batch(nblk) - 1) / norm_batch(nblk)); }
 
-// Blocks that walk the rows: as many as the SMs hold with `per_sm` threads each
-long long norm_grid(long long rows, int D, int per_sm) {
-    const int sms = sm_count(), threads = norm_threads(blocks_of(D));
+// Blocks that walk the rows: as many as the SMs hold
+long long norm_grid(long long rows, int D) {
+    const int sms = sm_count(), threads = norm_threads(blocks_of(D)), per_sm = norm_sm_threads(norm_batch(blocks_of(D)));
     if (sms <= 0) return 0;
     const long long most = (long long)sms * (per_sm / threads > 0 ? per_sm / threads : 1);
     return rows < most ? rows : most;
 }
-constexpr int kNormThreads = 1024;      // on an SM, at 64 registers a thread
 
 template <typename K, typename P>
 wkv7_status norm_launch(K kernel, const P &p, long long grid, int threads, size_t smem, cudaStream_t st) {
@@ -387,13 +504,23 @@ wkv7_status norm_launch(K kernel, const P &p, long long grid, int threads, size_
     kernel<<<(unsigned)grid, threads, smem, st>>>(p);
     return launch_status();
 }
-// blocks of 128 a warp as a template argument
-#define WKV7_NORM_MB(V, R)                    \
-    do {                                      \
-        if (mb == 1) WKV7_NORM(V, 1, R);      \
-        else if (mb == 2) WKV7_NORM(V, 2, R); \
-        else WKV7_NORM(V, 4, R);              \
-    } while (0)
+// blocks of 128 a warp as a template argument; rows ahead where vector accesses
+// are allowed and an SM's shared memory holds them
+template <bool VEC, bool WIDE, typename F> wkv7_status by_batch(int nblk, int tensors, F &&f) {
+    constexpr size_t kMost = 200 * 1024;
+    auto ring = [&](auto mb) {
+        if constexpr (VEC) {
+            if (ring_bytes<decltype(mb)::value, WIDE>(tensors, norm_threads(nblk)) <= kMost) return f(mb, std::true_type{});
+        }
+        return f(mb, std::false_type{});
+    };
+    switch (norm_batch(nblk)) {
+        case 1: return ring(std::integral_constant<int, 1>{});
+        case 2: return ring(std::integral_constant<int, 2>{});
+        case 4: return ring(std::integral_constant<int, 4>{});
+    }
+    return f(std::integral_constant<int, 8>{}, std::false_type{});
+}
 
 wkv7_status norm_dims(long long rows, int D) {
     if (rows < 0 || D < 0) return WKV7_ERR_INVALID_ARG;
@@ -452,27 +579,28 @@ wkv7_status wkv7_rmsnorm_forward(long long rows, int D, wkv7_dtype x_dt, wkv7_dt
     if ((s_codes != nullptr) != (s_scales != nullptr) || !f32_opt(s_scales)) return WKV7_ERR_INVALID_ARG;
     const NormFwd P{rows, D, x_dt, r_dt, y_dt, x, x_ld, residual, weight, (double)eps, 1.0 / D, residual_out, y,
                     y_scales, (uint8_t *)s_codes, s_scales, rstd};
-    const long long grid = norm_grid(rows, D, kNormThreads);
+    const long long grid = norm_grid(rows, D);
     if (grid <= 0) return WKV7_ERR_CUDA;
     const bool vec = D % 4 == 0 && x_ld % 4 == 0 && aligned_to(x, 4 * dtype_size(x_dt)) &&
                      aligned_to(residual, 4 * dtype_size(r_dt)) && aligned_to(residual_out, 4 * dtype_size(r_dt)) &&
                      aligned_to(y, 4 * dtype_size(y_dt)) && aligned_to(weight, 16) && aligned_to(s_codes, 4);
-    const int mb = norm_batch(blocks_of(D)), threads = norm_threads(blocks_of(D));
+    const int nblk = blocks_of(D), threads = norm_threads(nblk);
     const bool narrow = x_dt == WKV7_BF16 && (!residual || r_dt == WKV7_BF16);
-    wkv7_status done = WKV7_OK;
-#define WKV7_NORM(V, M, R) \
-    done = norm_launch(rmsnorm_fwd_kernel<V, M, R>, P, grid, threads, V && M <= 2 ? ring_bytes<M, R>(2, threads) : 0, stream)
-    if (vec && narrow) WKV7_NORM_MB(true, false);
-    else if (vec) WKV7_NORM_MB(true, true);
-    else WKV7_NORM_MB(false, true);
+#define WKV7_NORM(V, R)                                                                                     \
+    by_batch<V, R>(nblk, 2, [&](auto mb, auto ring) {                                                       \
+        constexpr int M = decltype(mb)::value;                                                              \
+        constexpr bool G = decltype(ring)::value;                                                           \
+        return norm_launch(rmsnorm_fwd_kernel<V, M, R, G>, P, grid, threads,                                \
+                           G ? ring_bytes<M, R>(2, threads) : 0, stream);                                   \
+    })
+    return vec && narrow ? WKV7_NORM(true, false) : vec ? WKV7_NORM(true, true) : WKV7_NORM(false, true);
 #undef WKV7_NORM
-    return done;
 }
 
 size_t wkv7_rmsnorm_backward_workspace_size(long long rows, int D) {
     using namespace wkv7::mixer;
     if (rows <= 0 || D <= 0 || norm_dims(rows, D) != WKV7_OK) return 0;
-    return (size_t)norm_grid(rows, D, kNormThreads) * D * sizeof(float);
+    return (size_t)norm_grid(rows, D) * D * sizeof(float);
 }
 
 wkv7_status wkv7_rmsnorm_backward(long long rows, int D, wkv7_dtype s_dt, wkv7_dtype dy_dt, wkv7_dtype g_dt,
@@ -492,7 +620,7 @@ wkv7_status wkv7_rmsnorm_backward(long long rows, int D, wkv7_dtype s_dt, wkv7_d
         (dresidual && !elem_ok(dresidual, g_dt)))
         return WKV7_ERR_INVALID_ARG;
     if ((s_dt == WKV7_E4M3) != (s_scales != nullptr) || !f32_opt(s_scales)) return WKV7_ERR_INVALID_ARG;
-    const long long grid = norm_grid(rows, D, kNormThreads);
+    const long long grid = norm_grid(rows, D);
     if (grid <= 0) return WKV7_ERR_CUDA;
     if (workspace == nullptr || !aligned_to(workspace, 16) || workspace_bytes < (size_t)grid * D * sizeof(float))
         return WKV7_ERR_INVALID_ARG;
@@ -501,15 +629,17 @@ wkv7_status wkv7_rmsnorm_backward(long long rows, int D, wkv7_dtype s_dt, wkv7_d
     const bool vec = D % 4 == 0 && aligned_to(s, 4 * dtype_size(s_dt)) && aligned_to(dy, 4 * dtype_size(dy_dt)) &&
                      aligned_to(dresidual, 4 * dtype_size(g_dt)) && aligned_to(dx, 4 * dtype_size(g_dt)) &&
                      aligned_to(weight, 16);
-    const int mb = norm_batch(blocks_of(D)), threads = norm_threads(blocks_of(D));
+    const int nblk = blocks_of(D), threads = norm_threads(nblk);
     const bool narrow = s_dt != WKV7_F32 && dy_dt == WKV7_BF16 && (!dresidual || g_dt == WKV7_BF16);
-    wkv7_status done = WKV7_OK;
-#define WKV7_NORM(V, M, R)                                                                                      \
-    done = norm_launch(rmsnorm_bwd_kernel<V, M, R>, P, grid, threads,                                           \
-                       M > 2 ? (size_t)4 * M * threads * sizeof(float) : V ? ring_bytes<M, R>(3, threads) : 0, stream)
-    if (vec && narrow) WKV7_NORM_MB(true, false);
-    else if (vec) WKV7_NORM_MB(true, true);
-    else WKV7_NORM_MB(false, true);
+#define WKV7_NORM(V, R)                                                                                     \
+    by_batch<V, R>(nblk, 3, [&](auto mb, auto ring) {                                                       \
+        constexpr int M = decltype(mb)::value;                                                              \
+        constexpr bool G = decltype(ring)::value;                                                           \
+        return norm_launch(rmsnorm_bwd_kernel<V, M, R, G>, P, grid, threads,                                \
+                           G ? ring_bytes<M, R>(3, threads) : M > 4 ? (size_t)4 * M * threads * sizeof(float) : 0, \
+                           stream);                                                                         \
+    })
+    const wkv7_status done = vec && narrow ? WKV7_NORM(true, false) : vec ? WKV7_NORM(true, true) : WKV7_NORM(false, true);
 #undef WKV7_NORM
     if (done != WKV7_OK) return done;
     sum_parts(grid, D, (const float *)workspace, dweight, stream);

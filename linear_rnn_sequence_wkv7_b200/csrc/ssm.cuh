@@ -43,7 +43,13 @@ struct ScanArgs {
     float *seg_end, *seg_dt;        // summaries: end state from zero, sum of dt
 };
 
-__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+// volatile: the compiler keeps their order, and with it the distance to their use
+__device__ __forceinline__ float ex2_ahead(float x) {
+    float y;
+    asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2_ahead(x.x), ex2_ahead(x.y)); }
 
 // Four n of a token's B or C; `left`: how many are there
 template <typename T, bool VEC> struct Quad {
