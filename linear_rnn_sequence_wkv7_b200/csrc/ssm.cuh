@@ -61,6 +61,17 @@ template <typename T, bool VEC> struct Quad {
             if (i < left) v[i].load(p + i);
         }
     }
+    __device__ __forceinline__ void get(float (&f)[4]) const {
+        if constexpr (VEC) v[0].get(f);
+        else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float g[1];
+                v[i].get(g);
+                f[i] = g[0];
+            }
+        }
+    }
     // to shared memory, in the order 0 xor p, 1 xor p, ...
     __device__ __forceinline__ void put(float *to, int p = 0) const {
         uint32_t w[4];

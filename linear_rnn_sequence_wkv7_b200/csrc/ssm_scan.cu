@@ -339,10 +339,11 @@ ssm_chain_kernel(long long total, int N, int nseg, const float *__restrict__ A, 
 }
 
 // One token: LN lanes a channel, 4 n a lane.  Bound by the state's read and
-// write, 8 bytes an n.
+// write, 8 bytes an n.  R = 4: a thread takes the same channel of four sequences,
+// so that four states are on their way and the rates are read once for them.
 struct StepArgs {
-    long long total;                // B * D
-    int D, N, G, Dg;
+    int B, D, N, Dg;
+    long long total;                // ceil(B / R) * D
     const void *u, *delta, *Bm, *Cm, *z;
     long long u_bs, d_bs, b_bs, c_bs, z_bs;
     const float *A, *Dskip, *dt_bias;
@@ -351,57 +352,95 @@ struct StepArgs {
     void *y;
 };
 
-template <typename T, typename YT, int LN, bool VEC>
-__global__ void __launch_bounds__(256)
+template <typename T, typename YT, int LN, int R, bool VEC>
+__global__ void __launch_bounds__(256, 4)
 ssm_step_kernel(const StepArgs P) {
     constexpr bool PRECISE = sizeof(YT) == 4;
-    const long long ch = ((long long)blockIdx.x * 256 + threadIdx.x) / LN;
+    const long long unit = ((long long)blockIdx.x * 256 + threadIdx.x) / LN;
     const int nl = threadIdx.x % LN, ns = 4 * nl;
-    if (ch >= P.total) return;                  // LN lanes leave together
-    const long long b = ch / P.D;
-    const int d = (int)(ch % P.D), g = d / P.Dg;
-    float *S = P.state + (size_t)ch * P.N + ns;
-    const float *A = P.A + (size_t)d * P.N + ns;
-    float h[4], a[4], Bv[4], Cv[4];
-    const T *Bm = static_cast<const T *>(P.Bm) + b * P.b_bs + g * P.N + ns;
-    const T *Cm = static_cast<const T *>(P.Cm) + b * P.c_bs + g * P.N + ns;
-    if constexpr (VEC) {                        // N = 4 LN
-        const float4 s4 = __ldcs(reinterpret_cast<const float4 *>(S)), a4 = __ldg(reinterpret_cast<const float4 *>(A));
-        h[0] = s4.x, h[1] = s4.y, h[2] = s4.z, h[3] = s4.w;
-        a[0] = a4.x, a[1] = a4.y, a[2] = a4.z, a[3] = a4.w;
-    }
+    if (unit >= P.total) return;                // LN lanes leave together
+    const long long b0 = unit / P.D * R;
+    const int d = (int)(unit % P.D), g = d / P.Dg, rows = (int)min((long long)R, P.B - b0);
+    // the softplus and the gate of row r are lane r's (of rows nl, nl + LN, ... where lanes are fewer)
+    constexpr int OWN = R > LN ? R / LN : 1;
+    float4 h[R];
+    Vec<T, 1> u[OWN], de[OWN], z[OWN];
+    Quad<T, VEC> Bq[R], Cq[R];
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        const bool in = VEC || ns + n < P.N;
-        if constexpr (!VEC) h[n] = in ? S[n] : 0.f, a[n] = in ? __ldg(A + n) : 0.f;
-        Bv[n] = in ? to_f32(Bm[n]) : 0.f;
-        Cv[n] = in ? to_f32(Cm[n]) : 0.f;
-    }
-    const float u = to_f32(static_cast<const T *>(P.u)[b * P.u_bs + d]);
-    const float x = to_f32(static_cast<const T *>(P.delta)[b * P.d_bs + d]) + (P.dt_bias ? __ldg(P.dt_bias + d) : 0.f);
-    const float dt = P.softplus ? softplus<sizeof(T) == 4>(x) : x, du = dt * u;
-    float y = 0.f;
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-        h[n] = fmaf(ex2(dt * (a[n] * kLog2e)), h[n], du * Bv[n]);
-        y = fmaf(h[n], Cv[n], y);
-    }
-    if constexpr (VEC) __stcs(reinterpret_cast<float4 *>(S), make_float4(h[0], h[1], h[2], h[3]));
-    else {
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-            if (ns + n < P.N) S[n] = h[n];
-    }
-    const unsigned group = ((LN == 32 ? 0u : (1u << LN)) - 1u) << (threadIdx.x & 31 & ~(LN - 1));
-#pragma unroll
-    for (int o = 1; o < LN; o <<= 1) y += __shfl_xor_sync(group, y, o);
-    if (nl == 0) {
-        if (P.Dskip) y = fmaf(__ldg(P.Dskip + d), u, y);
-        if (P.z) {
-            const float z = to_f32(static_cast<const T *>(P.z)[b * P.z_bs + d]);
-            y *= z * sigmoid<PRECISE>(z);
+    for (int r = 0; r < R; ++r) {
+        const long long b = r < rows ? b0 + r : b0;
+        const float *S = P.state + ((size_t)b * P.D + d) * P.N + ns;
+        if constexpr (VEC) h[r] = __ldcs(reinterpret_cast<const float4 *>(S));     // N = 4 LN
+        else {
+            h[r].x = ns < P.N ? S[0] : 0.f, h[r].y = ns + 1 < P.N ? S[1] : 0.f;
+            h[r].z = ns + 2 < P.N ? S[2] : 0.f, h[r].w = ns + 3 < P.N ? S[3] : 0.f;
         }
-        static_cast<YT *>(P.y)[ch] = from_f32<YT>(y);
+    }
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        const int r = (nl + i * LN) % R;
+        const long long b = r < rows ? b0 + r : b0;
+        u[i].load(static_cast<const T *>(P.u) + b * P.u_bs + d);
+        de[i].load(static_cast<const T *>(P.delta) + b * P.d_bs + d);
+        z[i].zero();
+        if (P.z) z[i].load(static_cast<const T *>(P.z) + b * P.z_bs + d);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const long long b = r < rows ? b0 + r : b0;
+        Bq[r].load(static_cast<const T *>(P.Bm) + b * P.b_bs + g * P.N + ns, P.N - ns);
+        Cq[r].load(static_cast<const T *>(P.Cm) + b * P.c_bs + g * P.N + ns, P.N - ns);
+    }
+    float2 a2[2];
+    load_rates(P.A + (size_t)d * P.N, P.N, ns, true, a2);
+    const float bias = P.dt_bias ? __ldg(P.dt_bias + d) : 0.f, skip = P.Dskip ? __ldg(P.Dskip + d) : 0.f;
+    const unsigned lane = threadIdx.x & 31, first = lane & ~(LN - 1), group = ((1u << LN) - 1u) << first;
+    float dts[OWN], us[OWN], ws[OWN];
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        float fu[1], fd[1];
+        u[i].get(fu), de[i].get(fd);
+        const float x = fd[0] + bias;
+        dts[i] = P.softplus ? softplus<sizeof(T) == 4>(x) : x;
+        us[i] = fu[0], ws[i] = dts[i] * fu[0];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        float B[4], C[4];
+        Bq[r].get(B), Cq[r].get(C);
+        float dt = dts[r / LN], w = ws[r / LN];
+        if constexpr (R > 1) {
+            dt = __shfl_sync(group, dt, first + r % LN);
+            w = __shfl_sync(group, w, first + r % LN);
+        }
+        const float2 d2 = make_float2(dt, dt), w2 = make_float2(w, w);
+        const float2 lo = __ffma2_rn(ex2(__fmul2_rn(d2, a2[0])), make_float2(h[r].x, h[r].y),
+                                     __fmul2_rn(w2, make_float2(B[0], B[1])));
+        const float2 hi = __ffma2_rn(ex2(__fmul2_rn(d2, a2[1])), make_float2(h[r].z, h[r].w),
+                                     __fmul2_rn(w2, make_float2(B[2], B[3])));
+        const float2 p = __ffma2_rn(hi, make_float2(C[2], C[3]), __fmul2_rn(lo, make_float2(C[0], C[1])));
+        float y = p.x + p.y;
+#pragma unroll
+        for (int o = 1; o < LN; o <<= 1) y += __shfl_xor_sync(group, y, o);
+        if (r >= rows) continue;
+        const size_t at = (size_t)(b0 + r) * P.D + d;
+        float *S = P.state + at * P.N + ns;
+        if constexpr (VEC) __stcs(reinterpret_cast<float4 *>(S), make_float4(lo.x, lo.y, hi.x, hi.y));
+        else {
+            const float v[4] = {lo.x, lo.y, hi.x, hi.y};
+#pragma unroll
+            for (int n = 0; n < 4; ++n)
+                if (ns + n < P.N) S[n] = v[n];
+        }
+        if (nl == r % LN) {
+            float fz[1];
+            y = fmaf(skip, us[r / LN], y);
+            if (P.z) {
+                z[r / LN].get(fz);
+                y *= fz[0] * sigmoid<PRECISE>(fz[0]);
+            }
+            static_cast<YT *>(P.y)[at] = from_f32<YT>(y);
+        }
     }
 }
 
@@ -572,15 +611,22 @@ wkv7_status wkv7_ssm_step(int B, int D, int N, int G, wkv7_dtype in_dt, wkv7_dty
         !aligned_to(z, dtype_size(in_dt)) || !f32_ok(A) || !f32_opt(Dskip) || !f32_opt(dt_bias) ||
         !elem_ok(y, y_dt) || state == nullptr || !aligned_to(state, 16))
         return WKV7_ERR_INVALID_ARG;
-    const StepArgs P{(long long)B * D, D, N, G, D / G, u, delta, Bm, Cm, z, u_bs, d_bs, b_bs, c_bs, z_bs, A, Dskip,
-                     dt_bias, state, softplus, y};
+    // four sequences a thread where that still makes two blocks an SM
+    const int lanes = scan_pad(N) / 4;
+    const bool four = (long long)((B + 3) / 4) * D * lanes >= 512ll * sm_count();
+    const StepArgs P{B, D, N, D / G, (four ? (long long)((B + 3) / 4) : B) * D, u, delta, Bm, Cm, z, u_bs, d_bs,
+                     b_bs, c_bs, z_bs, A, Dskip, dt_bias, state, softplus, y};
+    const size_t quad = 4 * dtype_size(in_dt);
+    const bool quads = (b_bs | c_bs) % 4 == 0 && aligned_to(Bm, quad) && aligned_to(Cm, quad);
     by_pad(scan_pad(N), [&](auto np) {
         constexpr int LN = decltype(np)::value / 4;
         const unsigned grid = (unsigned)((P.total * LN + 255) / 256);
-        const bool vec = N == 4 * LN && aligned_to(A, 16);
+        const bool vec = N == 4 * LN && quads;
 #define WKV7_STEP(I, O)                                                                 \
-    (vec ? (void)(ssm_step_kernel<I, O, LN, true><<<grid, 256, 0, stream>>>(P))         \
-         : (void)(ssm_step_kernel<I, O, LN, false><<<grid, 256, 0, stream>>>(P)))
+    (four ? (vec ? (void)(ssm_step_kernel<I, O, LN, 4, true><<<grid, 256, 0, stream>>>(P))    \
+                 : (void)(ssm_step_kernel<I, O, LN, 4, false><<<grid, 256, 0, stream>>>(P)))  \
+          : (vec ? (void)(ssm_step_kernel<I, O, LN, 1, true><<<grid, 256, 0, stream>>>(P))    \
+                 : (void)(ssm_step_kernel<I, O, LN, 1, false><<<grid, 256, 0, stream>>>(P))))
         if (in_dt == WKV7_F32 && y_dt == WKV7_F32) WKV7_STEP(float, float);
         else if (in_dt == WKV7_F32) WKV7_STEP(float, bf16);
         else if (y_dt == WKV7_F32) WKV7_STEP(bf16, float);

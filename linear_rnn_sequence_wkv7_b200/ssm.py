@@ -117,42 +117,44 @@ def _on(t: torch.Tensor, stream):
     """Context in which a call on ``t``'s device allocates and launches."""
     if not t.is_cuda:
         raise ValueError("tensors must be CUDA tensors")
+    if stream is None and t.get_device() == torch.cuda.current_device():
+        return _here
     if stream is not None and stream.device != t.device:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {t.device}")
-    if stream is None and t.device.index == torch.cuda.current_device():
-        return _here
     return _entered(t.device, stream)
 
 
 def _raw(t: torch.Tensor) -> int:
-    """The current stream of the (now current) device."""
-    return torch.cuda.current_stream(t.device).cuda_stream
+    """The current stream of ``t``'s (now current) device."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _full(t, shape, dtype, dev, name):
     """Pointer of a contiguous tensor of that shape and type (None stays None)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
-    if t.device != dev or not t.is_contiguous():
+    if t.get_device() != dev.index or not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous and on {dev}")
     return t.data_ptr()
 
 
 def _tokens(t, shape, dtype, dev, name, inner=1):
     """Pointer and strides of a per-token input, whose last ``inner`` dimensions are contiguous."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name}: expected {tuple(shape)} {dtype}, got {tuple(t.shape)} {t.dtype}")
     st = t.stride()
-    if t.device != dev or (shape[-1] > 1 and st[-1] != 1) or (inner == 2 and shape[-2] > 1 and st[-2] != shape[-1]):
+    if t.get_device() != dev.index or (st[-1] != 1 and shape[-1] > 1) or (inner == 2 and st[-2] != shape[-1] and shape[-2] > 1):
         raise ValueError(f"{name}: a token's channels must be contiguous, on {dev}")
-    return (t.data_ptr(),) + tuple(st[:len(shape) - inner])
+    return (t.data_ptr(), *st[:-inner])
 
 
 def _rows(t: torch.Tensor, name: str):
     """(rows, stride between rows) of a [..., D] tensor whose rows are evenly spaced."""
     D = t.shape[-1]
+    if t.is_contiguous():
+        return (t.numel() // D if D else 0), D
     if D > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name}: a row's channels must be contiguous")
     rows, ld, reach = 1, D, None
@@ -174,14 +176,14 @@ def _blocks(D: int) -> int:
 
 def _new_act8(shape, dev) -> Act8:
     return Act8(torch.empty(shape, dtype=CODE_DTYPE, device=dev),
-                torch.empty(tuple(shape[:-1]) + (_blocks(shape[-1]),), dtype=torch.float32, device=dev))
+                torch.empty((*shape[:-1], _blocks(shape[-1])), dtype=torch.float32, device=dev))
 
 
 def _act8_ptrs(a, shape, dev, name):
     if a is None:
         return None, None
     return (_full(a.codes, shape, CODE_DTYPE, dev, name + ".codes"),
-            _full(a.scales, tuple(shape[:-1]) + (_blocks(shape[-1]),), torch.float32, dev, name + ".scales"))
+            _full(a.scales, (*shape[:-1], _blocks(shape[-1])), torch.float32, dev, name + ".scales"))
 
 
 def _workspace(ws, nbytes, dev):
@@ -210,8 +212,10 @@ def act8_save(x, *, out: Optional[Act8] = None, stream=None) -> Act8:
     rows, ld = _rows(x, "x")
     with _on(x, stream):
         if out is None:
-            out = _new_act8(tuple(x.shape), x.device)
-        c, s = _act8_ptrs(out, x.shape, x.device, "out")
+            out = _new_act8(x.shape, x.device)
+            c, s = out.codes.data_ptr(), out.scales.data_ptr()
+        else:
+            c, s = _act8_ptrs(out, x.shape, x.device, "out")
         st = lib.wkv7_act8_save(rows, x.shape[-1], dt, x.data_ptr(), ld, c, s, _raw(x))
         _done("wkv7_act8_save", st, stream)
     return out
@@ -221,14 +225,16 @@ def act8_load(a: Act8, dtype=torch.bfloat16, *, out=None, stream=None):
     """The values [..., D] that 8-bit codes stand for (exact in bf16 and fp32)."""
     lib = load_library()
     dtype = _out_dtype(dtype, torch.bfloat16)
-    shape, dev = tuple(a.codes.shape), a.codes.device
+    shape, dev = a.codes.shape, a.codes.device
     with _on(a.codes, stream):
         if out is None:
             out = torch.empty(shape, dtype=dtype, device=dev)
+            op = out.data_ptr()
+        else:
+            op = _full(out, shape, dtype, dev, "out")
         c, s = _act8_ptrs(a, shape, dev, "a")
         D = shape[-1]
-        st = lib.wkv7_act8_load(a.codes.numel() // D if D else 0, D, c, s, _CODE[dtype],
-                                _full(out, shape, dtype, dev, "out"), _raw(out))
+        st = lib.wkv7_act8_load(a.codes.numel() // D if D else 0, D, c, s, _CODE[dtype], op, _raw(out))
         _done("wkv7_act8_load", st, stream)
     return out
 
@@ -245,7 +251,8 @@ def rmsnorm_forward(x, weight, residual=None, *, eps=1e-6, out8=False, save8=Fal
     in the residual's dtype (None without a residual; ``residual_out`` may be
     ``residual`` itself), ``rstd`` [...] fp32."""
     lib = load_library()
-    dev, shape, D = x.device, tuple(x.shape), x.shape[-1]
+    dev, shape = x.device, x.shape
+    D = shape[-1]
     rows, ld = _rows(x, "x")
     xc = _code(x)
     rc = xc if residual is None else _code(residual)
@@ -253,13 +260,17 @@ def rmsnorm_forward(x, weight, residual=None, *, eps=1e-6, out8=False, save8=Fal
         raise ValueError("y_dtype: not with out8")
     with _on(x, stream):
         if out8:
-            y = _new_act8(shape, dev) if y is None else y
-            yc, (yp, ysp) = E4M3, _act8_ptrs(y, shape, dev, "y")
+            yc = E4M3
+            if y is None:
+                y = _new_act8(shape, dev)
+                yp, ysp = y.codes.data_ptr(), y.scales.data_ptr()
+            else:
+                yp, ysp = _act8_ptrs(y, shape, dev, "y")
         else:
             y = torch.empty(shape, dtype=_out_dtype(y_dtype, x.dtype), device=dev) if y is None else y
             yc, yp, ysp = _code(y), _full(y, shape, y.dtype, dev, "y"), None
         if residual is not None and residual_out is None:
-            residual_out = torch.empty(shape, dtype=residual.dtype, device=dev)
+            residual_out = torch.empty_like(residual)
         if residual is None and residual_out is not None:
             raise ValueError("residual_out: only with a residual")
         if save8 and saved is None:
@@ -366,10 +377,12 @@ def conv_step(x, weight, bias, state, *, silu=True, y=None, y_dtype=None, stream
     with _on(x, stream):
         if y is None:
             y = torch.empty((B, D), dtype=_out_dtype(y_dtype, x.dtype), device=dev)
+            yp = y.data_ptr()
+        else:
+            yp = _full(y, (B, D), y.dtype, dev, "y")
         st = lib.wkv7_conv_step(B, D, W, _code(x), _code(y), xp, xb, _full(weight, (D, W), torch.float32, dev, "weight"),
                                 _full(bias, (D,), torch.float32, dev, "bias"),
-                                _full(state, (B, W - 1, D), x.dtype, dev, "state"), int(silu),
-                                _full(y, (B, D), y.dtype, dev, "y"), _raw(x))
+                                _full(state, (B, W - 1, D), x.dtype, dev, "state"), silu, yp, _raw(x))
         _done("wkv7_conv_step", st, stream)
     return y
 
@@ -492,9 +505,11 @@ def ssm_step(u, delta, A, B, C, state, D=None, z=None, dt_bias=None, *, softplus
         Dn, N, G, args = _scan_args(u, delta, A, B, C, D, z, dt_bias)
         if y is None:
             y = torch.empty((Bn, Dn), dtype=_out_dtype(y_dtype, u.dtype), device=dev)
+            yp = y.data_ptr()
+        else:
+            yp = _full(y, (Bn, Dn), y.dtype, dev, "y")
         st = lib.wkv7_ssm_step(Bn, Dn, N, G, _code(u), _code(y), *args,
-                               _full(state, (Bn, Dn, N), torch.float32, dev, "state"), int(softplus),
-                               _full(y, (Bn, Dn), y.dtype, dev, "y"), _raw(u))
+                               _full(state, (Bn, Dn, N), torch.float32, dev, "state"), softplus, yp, _raw(u))
         _done("wkv7_ssm_step", st, stream)
     return y
 
