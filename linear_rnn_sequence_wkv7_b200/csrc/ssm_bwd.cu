@@ -7,14 +7,18 @@
 //     d(dt)_t = u_t sum_n g_t B_t + sum_n A p_t g_t,   ddelta = d(dt) softplus'
 //     dA = sum_t dt_t p_t g_t       dD = sum ds u       dz = dy s (z sigmoid(z))'
 //
-// A thread holds 4 n of one channel, the lanes of a channel side by side, 256
+// A thread holds 4 n of two channels, the lanes of a channel side by side, 128
 // threads a block (64 channels at N = 16).  A block walks its tiles of 16 tokens
 // from the last to the first, each in two halves: from the state saved before the
-// tile it replays the half's 8 tokens with every h in registers (32; all 16 tokens
-// at once spilled at the 128 registers that two blocks an SM allow), then runs the
-// adjoint back over them.  Bound: 2.5 exponentials per (token, channel, n), 1.5 in
-// the replays and one on the way back, and about as many cycles of issue: some 80
-// instructions a warp for 8 channels of a token.
+// tile it replays the half's 8 tokens with every h in registers, then runs the
+// adjoint back over them.  2.5 exponentials per (token, channel, n), 1.5 in the
+// replays and one on the way back.
+//
+// 4 x 4096 tokens x 2048 channels, N = 16, bf16: 0.94 ms in two segments, plus
+// 0.22 ms for their summaries.  Bound by latency: two warps a scheduler is what
+// 255 registers leave, each issues once in four cycles (all 16 tokens at once
+// spilled; one channel a thread with twice the warps 0.99 ms; three blocks an SM
+// at 168 registers spilled too, 1.04 ms).
 //
 // Sums over n (C . h, g . B, A . p g) go to shared memory lane by lane and are
 // added up by the threads that write the outputs.  Sums over channels (dB, dC) run
@@ -169,8 +173,8 @@ ssm_bwd_chain_kernel(long long total, int N, int nseg, const float *__restrict__
     }
 }
 
-constexpr int kBwdThreads = 256;
-__host__ __device__ constexpr int bwd_channels(int NP) { return kBwdThreads * 4 / NP; }      // of a block
+constexpr int kBwdThreads = 128, kBwdTC = 2;        // channels a thread
+__host__ __device__ constexpr int bwd_channels(int NP) { return kBwdTC * kBwdThreads * 4 / NP; }     // of a block
 
 // slots <-> n: slot j holds n = j xor p, p = 0 .. 3; its own inverse
 __device__ __forceinline__ void permute(float2 (&v)[2], int p) {
@@ -191,19 +195,19 @@ template <typename T, int NP> struct BwdShared {
     static constexpr int GB = Y + Sum::FLOATS;                  // g . B
     static constexpr int AP = GB + Sum::FLOATS;                 // A . p g
     static constexpr int PART = AP + Sum::FLOATS;               // [WARPS][kTile][2][NP] dB, dC
-    static constexpr int DA = PART + WARPS * kTile * 2 * NP;    // [8][threads]: sums and their errors
-    static constexpr int ACC = DA + 8 * kBwdThreads;            // [2 V][threads]: dD, ddt_bias
-    static constexpr int FLOATS = ACC + 2 * (kTile / LN) * kBwdThreads;
+    static constexpr int DA = PART + WARPS * kTile * 2 * NP;    // [8 TC][threads]: sums and their errors
+    static constexpr int ACC = DA + 8 * kBwdTC * kBwdThreads;   // [2 V][threads]: dD, ddt_bias
+    static constexpr int FLOATS = ACC + 2 * 4 * kBwdThreads;
 };
 
 template <typename T, int NP, bool VEC>
-__global__ void __launch_bounds__(kBwdThreads, NP <= 32 ? 2 : 1)
+__global__ void __launch_bounds__(kBwdThreads, 2)
 ssm_bwd_kernel(const BwdArgs K) {
     const ScanArgs &P = K.f;
     using S = BwdShared<T, NP>;
     using Sum = typename S::Sum;
     constexpr int CC = S::CC, LN = S::LN, CG = 32 / LN, THREADS = kBwdThreads;      // CG channels a warp
-    constexpr int EPT = kTile / LN, V = VEC ? EPT : 1, Q = EPT / V;
+    constexpr int TC = kBwdTC, EPT = kTile * CC / THREADS, V = VEC ? (EPT < 4 ? EPT : 4) : 1, Q = EPT / V;
     constexpr int IB = 2 * kTile * NP / 4, NB = (IB + THREADS - 1) / THREADS;
     constexpr bool PRECISE = sizeof(T) == 4;
     extern __shared__ __align__(16) float smem[];
@@ -240,21 +244,24 @@ ssm_bwd_kernel(const BwdArgs K) {
         skip[i] = (live && P.Dskip) ? __ldg(P.Dskip + lc + i) : 0.f;
     }
 
-    const int nl = tid % LN, cl = tid / LN, cs = c0 + cl, ns = 4 * nl, cg = lane / LN, order = cg & 3;
-    const bool mine = cs < c1;
-    float2 a2[2], w[2];             // rates (log2), adjoint carried to the token before; by slots
-    load_rates(P.A + (size_t)cs * P.N, P.N, ns, mine, a2);
-    permute(a2, order);
-    w[0] = w[1] = make_float2(0.f, 0.f);
-    if (mine && K.exit) load_state(K.exit + (((size_t)seg * P.B + b) * P.D + cs) * P.N, P.N, ns, w);
-    permute(w, order);
+    const int nl = tid % LN, cl = tid / LN * TC, cs = c0 + cl, ns = 4 * nl, cg = lane / LN, order = cg & 3;
+    float2 a2[TC][2], w[TC][2];     // rates (log2), adjoint carried to the token before; by slots
+#pragma unroll
+    for (int c = 0; c < TC; ++c) {
+        const bool mine = cs + c < c1;
+        load_rates(P.A + (size_t)(cs + c) * P.N, P.N, ns, mine, a2[c]);
+        permute(a2[c], order);
+        w[c][0] = w[c][1] = make_float2(0.f, 0.f);
+        if (mine && K.exit) load_state(K.exit + (((size_t)seg * P.B + b) * P.D + cs + c) * P.N, P.N, ns, w[c]);
+        permute(w[c], order);
+    }
     for (int i = 0; i < 2 * V; ++i) s_acc[i * THREADS + tid] = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s_dA[i * THREADS + tid] = 0.f;
+    for (int i = 0; i < 8 * TC; ++i) s_dA[i * THREADS + tid] = 0.f;
 
     Vec<T, V> nu[Q], nd[Q], nz[Q], ng[Q], cu[Q], cd[Q], cz[Q], cy[Q];
     Quad<T, VEC> nb[NB];
-    float2 h0[2];
+    float2 h0[TC][2];
     auto fetch = [&](int t) {
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
@@ -300,9 +307,13 @@ ssm_bwd_kernel(const BwdArgs K) {
 #pragma unroll
             for (int p = 0; p < 4; ++p) nb[q].put(to + p * NP, p);
         }
-        h0[0] = h0[1] = make_float2(0.f, 0.f);
-        if (mine) load_state(P.states + ((size_t)(b * P.nck + t / kTile) * P.D + cs) * P.N, P.N, ns, h0);
-        permute(h0, order);
+#pragma unroll
+        for (int c = 0; c < TC; ++c) {
+            h0[c][0] = h0[c][1] = make_float2(0.f, 0.f);
+            if (cs + c < c1)
+                load_state(P.states + ((size_t)(b * P.nck + t / kTile) * P.D + cs + c) * P.N, P.N, ns, h0[c]);
+            permute(h0[c], order);
+        }
     };
 
     const int last = t0 + (t1 - 1 - t0) / kTile * kTile;
@@ -314,17 +325,29 @@ ssm_bwd_kernel(const BwdArgs K) {
     for (int t = last; t >= t0 && t1 > t0; t -= kTile) {
         if (t - kTile >= t0) fetch(t - kTile);
 
-        float2 dA[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float2 dA[TC][2];
+#pragma unroll
+        for (int c = 0; c < TC; ++c) dA[c][0] = dA[c][1] = make_float2(0.f, 0.f);
+        auto steps = [&](int k, float2 (&d2)[TC], float2 (&v2)[TC]) {      // dt and dt u of this thread's channels
+            const float4 q = *reinterpret_cast<const float4 *>(&s_dd[k][cl]);
+            d2[0] = make_float2(q.x, q.x), v2[0] = make_float2(q.y, q.y);
+            d2[1] = make_float2(q.z, q.z), v2[1] = make_float2(q.w, q.w);
+        };
 #pragma unroll 1
         for (int half = kTile / 2; half >= 0; half -= kTile / 2) {
         // ---- replay: the state up to the half, then every h of it
-        float2 h[kTile / 2][2], hs[2] = {h0[0], h0[1]};
-        auto advance = [&](int k, const float2 (&from)[2], float2 (&to)[2]) {
-            const float2 dd = s_dd[k][cl], d2 = make_float2(dd.x, dd.x), v2 = make_float2(dd.y, dd.y);
-            float2 B[2];
+        float2 h[kTile / 2][TC][2], hs[TC][2];
+#pragma unroll
+        for (int c = 0; c < TC; ++c) hs[c][0] = h0[c][0], hs[c][1] = h0[c][1];
+        auto advance = [&](int k, const float2 (&from)[TC][2], float2 (&to)[TC][2]) {
+            float2 d2[TC], v2[TC], B[2];
+            steps(k, d2, v2);
             shared_n(&s_BC[0][k][order][ns], B);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) to[j] = __ffma2_rn(ex2(__fmul2_rn(d2, a2[j])), from[j], __fmul2_rn(v2, B[j]));
+            for (int c = 0; c < TC; ++c)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    to[c][j] = __ffma2_rn(ex2(__fmul2_rn(d2[c], a2[c][j])), from[c][j], __fmul2_rn(v2[c], B[j]));
         };
         if (half) {
 #pragma unroll
@@ -337,30 +360,41 @@ ssm_bwd_kernel(const BwdArgs K) {
 #pragma unroll
         for (int i = kTile / 2 - 1; i >= 0; --i) {
             const int k = half + i;
-            const float2 dd = s_dd[k][cl], d2 = make_float2(dd.x, dd.x), v2 = make_float2(dd.y, dd.y);
-            const float e = s_ds[k][cl];
-            const float2 e2 = make_float2(e, e);
-            float2 B[2], C[2], gg[2], dB[2], dC[2], q[2];
+            float2 d2[TC], v2[TC], B[2], C[2], dB[2], dC[2];
+            steps(k, d2, v2);
+            const float2 e = *reinterpret_cast<const float2 *>(&s_ds[k][cl]);
+            const float2 e2[TC] = {make_float2(e.x, e.x), make_float2(e.y, e.y)};
             shared_n(&s_BC[0][k][order][ns], B);
             shared_n(&s_BC[1][k][order][ns], C);
             if (z) {
-                const float2 y = __ffma2_rn(h[i][1], C[1], __fmul2_rn(h[i][0], C[0]));
-                Sum::put(s_y, k, cl, nl, y.x + y.y);
-            }
+                float yc[TC];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float2 a = ex2(__fmul2_rn(d2, a2[j]));
-                gg[j] = __ffma2_rn(e2, C[j], w[j]);
-                w[j] = __fmul2_rn(a, gg[j]);
-                q[j] = __fmul2_rn(w[j], i ? h[i ? i - 1 : 0][j] : hs[j]);       // p g
-                dA[j] = __ffma2_rn(q[j], d2, dA[j]);
-                dB[j] = __fmul2_rn(v2, gg[j]);
-                dC[j] = __fmul2_rn(e2, h[i][j]);
+                for (int c = 0; c < TC; ++c) {
+                    const float2 y = __ffma2_rn(h[i][c][1], C[1], __fmul2_rn(h[i][c][0], C[0]));
+                    yc[c] = y.x + y.y;
+                }
+                Sum::template put<TC>(s_y, k, cl, nl, yc);
             }
-            const float2 gb = __ffma2_rn(gg[1], B[1], __fmul2_rn(gg[0], B[0]));
-            const float2 ap = __ffma2_rn(q[1], a2[1], __fmul2_rn(q[0], a2[0]));
-            Sum::put(s_gb, k, cl, nl, gb.x + gb.y);
-            Sum::put(s_ap, k, cl, nl, ap.x + ap.y);
+            float gbs[TC], aps[TC];
+#pragma unroll
+            for (int c = 0; c < TC; ++c) {
+                float2 gg[2], q[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float2 a = ex2(__fmul2_rn(d2[c], a2[c][j]));
+                    gg[j] = __ffma2_rn(e2[c], C[j], w[c][j]);
+                    w[c][j] = __fmul2_rn(a, gg[j]);
+                    q[j] = __fmul2_rn(w[c][j], i ? h[i ? i - 1 : 0][c][j] : hs[c][j]);      // p g
+                    dA[c][j] = __ffma2_rn(q[j], d2[c], dA[c][j]);
+                    dB[j] = c ? __ffma2_rn(v2[c], gg[j], dB[j]) : __fmul2_rn(v2[c], gg[j]);
+                    dC[j] = c ? __ffma2_rn(e2[c], h[i][c][j], dC[j]) : __fmul2_rn(e2[c], h[i][c][j]);
+                }
+                const float2 gb = __ffma2_rn(gg[1], B[1], __fmul2_rn(gg[0], B[0]));
+                const float2 ap = __ffma2_rn(q[1], a2[c][1], __fmul2_rn(q[0], a2[c][0]));
+                gbs[c] = gb.x + gb.y, aps[c] = ap.x + ap.y;
+            }
+            Sum::template put<TC>(s_gb, k, cl, nl, gbs);
+            Sum::template put<TC>(s_ap, k, cl, nl, aps);
             // over the warp's channels: lanes LN apart whose orders differ in one bit
             float bc[2][4] = {{dB[0].x, dB[0].y, dB[1].x, dB[1].y}, {dC[0].x, dC[0].y, dC[1].x, dC[1].y}};
 #pragma unroll
@@ -389,12 +423,16 @@ ssm_bwd_kernel(const BwdArgs K) {
         }
         }
         // the tile's part of dA, into a sum with its rounding error kept (two-sum)
-        const float tile_dA[4] = {dA[0].x, dA[0].y, dA[1].x, dA[1].y};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float s = s_dA[2 * i * THREADS + tid], x = tile_dA[i], n = s + x, v = n - s;
-            s_dA[2 * i * THREADS + tid] = n;
-            s_dA[(2 * i + 1) * THREADS + tid] += (s - (n - v)) + (x - v);
+        for (int c = 0; c < TC; ++c) {
+            const float tile_dA[4] = {dA[c][0].x, dA[c][0].y, dA[c][1].x, dA[c][1].y};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float *at = s_dA + (8 * c + 2 * i) * THREADS + tid;
+                const float s = at[0], x = tile_dA[i], n = s + x, v = n - s;
+                at[0] = n;
+                at[THREADS] += (s - (n - v)) + (x - v);
+            }
         }
         __syncthreads();
 
@@ -449,15 +487,18 @@ ssm_bwd_kernel(const BwdArgs K) {
     }
 
     const size_t part = (size_t)seg * P.B + b;
-    if (mine) {
-        permute(w, order);
-        if (seg == 0 && K.dstate0) store_state(K.dstate0 + ((size_t)b * P.D + cs) * P.N, P.N, ns, w);
+#pragma unroll
+    for (int c = 0; c < TC; ++c) {
+        if (cs + c >= c1) continue;
+        permute(w[c], order);
+        if (seg == 0 && K.dstate0) store_state(K.dstate0 + ((size_t)b * P.D + cs + c) * P.N, P.N, ns, w[c]);
         float v[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = s_dA[2 * i * THREADS + tid] + s_dA[(2 * i + 1) * THREADS + tid];
+        for (int i = 0; i < 4; ++i)
+            v[i] = s_dA[(8 * c + 2 * i) * THREADS + tid] + s_dA[(8 * c + 2 * i + 1) * THREADS + tid];
         float2 v2[2] = {make_float2(v[0], v[1]), make_float2(v[2], v[3])};
         permute(v2, order);
-        store_state(K.dA + (part * P.D + cs) * P.N, P.N, ns, v2);
+        store_state(K.dA + (part * P.D + cs + c) * P.N, P.N, ns, v2);
     }
     // dD and ddt_bias: the threads that loaded the same channels, in order
     __syncthreads();
