@@ -144,7 +144,7 @@ ssm_bwd_summary_kernel(const BwdArgs K) {
             float2 C[2];
             shared_n(&s_C[k][ns], C);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) w[j] = __fmul2_rn(ex2(__fmul2_rn(d2, a2[j])), __ffma2_rn(e2, C[j], w[j]));
+            for (int j = 0; j < 2; ++j) w[j] = __fmul2_rn(decay(d2, a2[j]), __ffma2_rn(e2, C[j], w[j]));
             part += dd.x;
         }
         sum += part;
@@ -347,7 +347,7 @@ ssm_bwd_kernel(const BwdArgs K) {
             for (int c = 0; c < TC; ++c)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
-                    to[c][j] = __ffma2_rn(ex2(__fmul2_rn(d2[c], a2[c][j])), from[c][j], __fmul2_rn(v2[c], B[j]));
+                    to[c][j] = __ffma2_rn(decay(d2[c], a2[c][j]), from[c][j], __fmul2_rn(v2[c], B[j]));
         };
         if (half) {
 #pragma unroll
@@ -381,7 +381,7 @@ ssm_bwd_kernel(const BwdArgs K) {
                 float2 gg[2], q[2];
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float2 a = ex2(__fmul2_rn(d2[c], a2[c][j]));
+                    const float2 a = decay(d2[c], a2[c][j]);
                     gg[j] = __ffma2_rn(e2[c], C[j], w[c][j]);
                     w[c][j] = __fmul2_rn(a, gg[j]);
                     q[j] = __fmul2_rn(w[c][j], i ? h[i ? i - 1 : 0][c][j] : hs[c][j]);      // p g

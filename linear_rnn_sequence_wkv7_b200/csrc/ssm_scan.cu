@@ -276,7 +276,7 @@ ssm_fwd_kernel(const ScanArgs P) {
                     const float2 d2 = make_float2(dt[c], dt[c]), w2 = make_float2(du[c], du[c]);
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
-                        av[i][c][m] = ex2(__fmul2_rn(d2, a2[c][m])), bv[i][c][m] = __fmul2_rn(w2, B[m]);
+                        av[i][c][m] = decay(d2, a2[c][m]), bv[i][c][m] = __fmul2_rn(w2, B[m]);
                     if constexpr (!Y) part[c] += dt[c];
                 }
             }
@@ -414,9 +414,9 @@ ssm_step_kernel(const StepArgs P) {
             w = __shfl_sync(group, w, first + r % LN);
         }
         const float2 d2 = make_float2(dt, dt), w2 = make_float2(w, w);
-        const float2 lo = __ffma2_rn(ex2(__fmul2_rn(d2, a2[0])), make_float2(h[r].x, h[r].y),
+        const float2 lo = __ffma2_rn(decay(d2, a2[0]), make_float2(h[r].x, h[r].y),
                                      __fmul2_rn(w2, make_float2(B[0], B[1])));
-        const float2 hi = __ffma2_rn(ex2(__fmul2_rn(d2, a2[1])), make_float2(h[r].z, h[r].w),
+        const float2 hi = __ffma2_rn(decay(d2, a2[1]), make_float2(h[r].z, h[r].w),
                                      __fmul2_rn(w2, make_float2(B[2], B[3])));
         const float2 p = __ffma2_rn(hi, make_float2(C[2], C[3]), __fmul2_rn(lo, make_float2(C[0], C[1])));
         float y = p.x + p.y;

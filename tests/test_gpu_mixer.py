@@ -454,6 +454,16 @@ def test_scan_backward_matches_differences(cuda_device):
             assert abs(float(flat[i]) - num) <= 1e-4 * (1 + abs(num)), (k, i)
 
 
+def test_scan_of_zero_steps_keeps_the_state_bit_for_bit(cuda_device):
+    v = scan_inputs(4, 2, 300, 40, 16, 1, "f32", bias=False)
+    v["delta"] = torch.zeros(2, 300, 40, device="cuda")
+    _, h = ssm.ssm_forward(**v, softplus=False)
+    assert torch.equal(h, v["state0"])
+    st = v["state0"].clone()
+    ssm.ssm_step(v["u"][:, 0], v["delta"][:, 0], v["A"], v["B"][:, 0], v["C"][:, 0], st, softplus=False)
+    assert torch.equal(st, v["state0"])
+
+
 def test_scan_strong_decay_and_large_steps(cuda_device):
     """Rates and steps at which exp(dt A) is 0, and delta far on both sides of the softplus."""
     v = scan_inputs(8, 1, 24, 32, 16, 1, "f32")
