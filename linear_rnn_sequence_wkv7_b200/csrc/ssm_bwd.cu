@@ -551,7 +551,9 @@ int bwd_tiles(int D, int N, int G) {
     return (D / G + CC - 1) / CC;
 }
 // Segments of a backward: two blocks an SM, if that makes at least two segments
-// (whose summaries cost about a third of a pass), each of at least 64 tokens.
+// (whose summaries cost about a fifth of a pass), each of at least 64 tokens.
+// N = 16, segments against one piece: 4 x 4096 x 2048 1.21 / 1.52 ms, 1 x 4096 x
+// 2048 0.30 / 1.45 ms, 1 x 256 x 2048 78 / 112 us.
 int bwd_segments(int B, int T, int D, int N, int G, int sms) {
     const long long blocks = (long long)B * G * bwd_tiles(D, N, G);
     if (blocks <= 0 || sms <= 0) return 1;

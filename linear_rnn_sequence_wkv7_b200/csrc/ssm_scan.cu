@@ -464,16 +464,20 @@ template <typename T, int NP, bool Y> void launch_fwd_tc(const ScanArgs &P, int 
 
 }  // namespace
 
-// Segments of a forward over B sequences: 16 scanning warps an SM at two channels
-// a thread, if that makes at least three segments (each token is then scanned
-// twice), each of at least 128 tokens.
+// Segments of a forward over B sequences.  One piece takes 0.04 us a token while
+// the SMs have up to two scanning warps each (0.05 at 3.5, 0.07 at 7); segments
+// scan each token twice, on as many warps as the SMs take.  So segments for 32
+// warps an SM where that makes twelve of them, and at least five of 128 tokens.
+// Bf16, N = 16, segments against one piece: 1 x 4096 x 2048 125 / 158 us, 2 x
+// 4096 x 2048 221 / 204, 1 x 1024 x 2048 46 / 45, 1 x 1024 x 256 23 / 42, 1 x 512
+// x 2048 43 / 30.
 int ssm_segments(int B, int T, int D, int N, int G, int sms) {
     const int NP = scan_pad(N), CC = scan_channels(NP), tiles = G > 0 ? (D / G + CC - 1) / CC : 0;
     const long long warps = (long long)B * G * tiles * scan_threads(NP, 1) / 32;
     if (warps <= 0 || sms <= 0) return 1;
     const long long want = 32ll * sms / warps, most = T / 128;
-    const long long s = want < most ? want : most;
-    return s >= 3 ? (int)s : 1;
+    if (want < 12 || most < 5) return 1;
+    return (int)(want < most ? want : most);
 }
 
 void ssm_fwd(const ScanArgs &P, wkv7_dtype dt, bool vec, bool y, cudaStream_t st) {
