@@ -52,7 +52,7 @@ template <typename T, bool VEC> struct Token {
 template <typename T, bool VEC> struct Stream {
     static constexpr bool ASYNC = VEC || sizeof(T) == 4;
     static constexpr int SLOT = 4 * (int)sizeof(T);
-    static constexpr int BYTES = ASYNC ? kConvRing * kConvGroup * (32 * SLOT + (sizeof(T) == 1 ? 4 : 0)) : 0;   // a warp
+    static constexpr int WARP_BYTES = ASYNC ? kConvRing * kConvGroup * (32 * SLOT + (sizeof(T) == 1 ? 4 : 0)) : 0;   // a warp
     unsigned char *base;
     Token<T, VEC> next[ASYNC ? 1 : kConvGroup];
     __device__ __forceinline__ unsigned char *slot(int i, int lane) const { return base + (i * 32 + lane) * SLOT; }
@@ -62,25 +62,36 @@ template <typename T, bool VEC> struct Stream {
     // group g of tokens from `row` on, `left` of them there (the others count as zero)
     __device__ __forceinline__ void fetch(int g, const T *row, long long ts, const float *scales, int nblk, int left,
                                           int blk, int lane, int D) {
+        if constexpr (!ASYNC) {
 #pragma unroll
-        for (int k = 0; k < kConvGroup; ++k) {
-            if constexpr (ASYNC) {
-                unsigned char *to = slot((g % kConvRing) * kConvGroup + k, lane);
-                if constexpr (VEC) {
-                    const int c = lane_channel<true>(blk, lane, 0);
-                    const bool in = k < left && c < D;
-                    copy_async<SLOT>(to, in ? row + k * ts + c : row, in);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int c = lane_channel<false>(blk, lane, i);
-                        const bool in = k < left && c < D;
-                        copy_async<(int)sizeof(T) < 4 ? 4 : (int)sizeof(T)>(to + 4 * i, in ? row + k * ts + c : row, in);
-                    }
-                }
-            } else {
+            for (int k = 0; k < kConvGroup; ++k) {
                 next[k].zero();
                 if (k < left) next[k].load(row + k * ts, scales + (long long)k * nblk, blk, lane, D);
+            }
+        } else {
+            unsigned char *to = slot((g % kConvRing) * kConvGroup, lane);
+            constexpr int PARTS = VEC ? 1 : 4, BYTES = SLOT / PARTS;
+            const T *p[PARTS];
+            bool there[PARTS];
+#pragma unroll
+            for (int i = 0; i < PARTS; ++i) {
+                const int c = lane_channel<VEC>(blk, lane, i);
+                there[i] = c < D;
+                p[i] = there[i] ? row + c : row;
+            }
+            if (VEC && left >= kConvGroup) {
+#pragma unroll
+                for (int k = 0; k < kConvGroup; ++k, p[0] += ts) copy_async<BYTES>(to + k * 32 * SLOT, p[0], there[0]);
+            } else {
+#pragma unroll
+            for (int k = 0; k < kConvGroup; ++k) {
+#pragma unroll
+                for (int i = 0; i < PARTS; ++i) {
+                    const bool in = there[i] && k < left;
+                    copy_async<BYTES>(to + k * 32 * SLOT + i * BYTES, k < left ? p[i] : row, in);
+                    p[i] += ts;
+                }
+            }
             }
         }
         if constexpr (ASYNC && sizeof(T) == 1) {
@@ -108,9 +119,12 @@ template <typename T, bool VEC> struct Stream {
                 }
                 r.get(v[k]);
                 if constexpr (sizeof(T) == 1) {
-                    const float f = *scale(i);
+                    const float2 f = make_float2(*scale(i), *scale(i));
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) v[k][c] *= f;
+                    for (int c = 0; c < 4; c += 2) {
+                        const float2 q = __fmul2_rn(make_float2(v[k][c], v[k][c + 1]), f);
+                        v[k][c] = q.x, v[k][c + 1] = q.y;
+                    }
                 }
             } else {
                 next[k].get(v[k]);
@@ -224,12 +238,13 @@ conv_fwd_kernel(const ConvFwd P) {
     uint8_t *pc = SAVE ? P.codes + row0 * D : nullptr;
     float *pq = SAVE ? P.scales + row0 * nblk + blk : nullptr;
     extern __shared__ __align__(16) unsigned char conv_smem[];
-    Stream<T, VEC> in{conv_smem + (threadIdx.x >> 5) * Stream<T, VEC>::BYTES};
+    Stream<T, VEC> in{conv_smem + (threadIdx.x >> 5) * Stream<T, VEC>::WARP_BYTES};
     constexpr bool ASYNC = Stream<T, VEC>::ASYNC;
-    auto fetch = [&](int g) {
+    auto fetch = [&](int g) {           // in order: the pointers go on from group to group
         const int t = t0 + g * kConvGroup;
-        if (t < t1) in.fetch(g, px + (long long)g * kConvGroup * P.x_ts, P.x_ts, ps + (long long)g * kConvGroup * nblk, nblk,
-                             t1 - t, blk, lane, D);
+        if (t < t1) in.fetch(g, px, P.x_ts, ps, nblk, t1 - t, blk, lane, D);
+        px += kConvGroup * P.x_ts;
+        if (sizeof(T) == 1) ps += (long long)kConvGroup * nblk;
         if constexpr (ASYNC) cp_async_commit();
     };
     fetch(0);
@@ -342,8 +357,8 @@ conv_bwd_kernel(const ConvBwd P) {
     constexpr bool PRECISE = sizeof(GT) == 4;
     __shared__ float part[kConvBwdWarps][W + 1][kBlk];
     extern __shared__ __align__(16) unsigned char conv_smem[];
-    Stream<T, VEC> xin{conv_smem + (threadIdx.x >> 5) * Stream<T, VEC>::BYTES};
-    Stream<DT, VEC> gin{conv_smem + kConvBwdWarps * Stream<T, VEC>::BYTES + (threadIdx.x >> 5) * Stream<DT, VEC>::BYTES};
+    Stream<T, VEC> xin{conv_smem + (threadIdx.x >> 5) * Stream<T, VEC>::WARP_BYTES};
+    Stream<DT, VEC> gin{conv_smem + kConvBwdWarps * Stream<T, VEC>::WARP_BYTES + (threadIdx.x >> 5) * Stream<DT, VEC>::WARP_BYTES};
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = P.D, nblk = (D + kBlk - 1) / kBlk;
     const int blk = (int)(blockIdx.x % nblk);
     const long long rest = blockIdx.x / nblk;
@@ -384,12 +399,18 @@ conv_bwd_kernel(const ConvBwd P) {
         constexpr bool ASYNC = Stream<T, VEC>::ASYNC && Stream<DT, VEC>::ASYNC;
         constexpr bool MIXED = !ASYNC && (Stream<T, VEC>::ASYNC || Stream<DT, VEC>::ASYNC);
         static_assert(!MIXED || !VEC, "vector accesses stream both");
+        const T *px = x + t0 * P.x_ts;
+        const float *ps = xs + (long long)t0 * nblk;
+        const DT *pg = dy + (long long)t0 * D;
         auto fetch = [&](int g) {
             const int t = t0 + g * kConvGroup;
             if (t < end) {
-                xin.fetch(g, x + t * P.x_ts, P.x_ts, xs + (long long)t * nblk, nblk, last - t, blk, lane, D);
-                gin.fetch(g, dy + (long long)t * D, D, nullptr, 0, last - t, blk, lane, D);
+                xin.fetch(g, px, P.x_ts, ps, nblk, last - t, blk, lane, D);
+                gin.fetch(g, pg, D, nullptr, 0, last - t, blk, lane, D);
             }
+            px += kConvGroup * P.x_ts;
+            pg += (long long)kConvGroup * D;
+            if (sizeof(T) == 1) ps += (long long)kConvGroup * nblk;
             if constexpr (ASYNC || MIXED) cp_async_commit();
         };
         fetch(0);
@@ -526,10 +547,10 @@ wkv7_status conv_dims(int B, int T, int D, int W) {
 }
 
 // Tokens a run: the fewer, the more a run's start (W - 1 tokens again, the weights)
-// costs, so 64 where that makes 32 warps an SM (8 x 4096 x 2048: 52 us), else 32 or
-// 16 (5 x 2999 x 531 in fp32: 7.4 us at 32, 11.9 at 64).
+// costs, so 64 where that makes 12 warps an SM (8 x 4096 x 2048: 52 us; 68 us at
+// 32), else 32 or 16.
 int conv_run(int B, int T, int D) {
-    const long long want = 32ll * sm_count();
+    const long long want = 12ll * sm_count();
     int run = 64;
     while (run > kConvMinRun && (long long)B * ((T + run - 1) / run) * blocks_of(D) < want) run /= 2;
     return run;
@@ -560,8 +581,8 @@ void launch_conv_fwd(const ConvFwd &P, int W, bool vec, cudaStream_t st) {
     const unsigned grid = (unsigned)((units + kConvWarps - 1) / kConvWarps);
     by_width(W, [&](auto w) {
         constexpr int WW = decltype(w)::value, th = 32 * kConvWarps;
-        if (vec) conv_launch(conv_fwd_kernel<T, ST, YT, WW, true, SAVE>, P, grid, th, kConvWarps * Stream<T, true>::BYTES, st);
-        else conv_launch(conv_fwd_kernel<T, ST, YT, WW, false, SAVE>, P, grid, th, kConvWarps * Stream<T, false>::BYTES, st);
+        if (vec) conv_launch(conv_fwd_kernel<T, ST, YT, WW, true, SAVE>, P, grid, th, kConvWarps * Stream<T, true>::WARP_BYTES, st);
+        else conv_launch(conv_fwd_kernel<T, ST, YT, WW, false, SAVE>, P, grid, th, kConvWarps * Stream<T, false>::WARP_BYTES, st);
     });
 }
 
@@ -572,10 +593,10 @@ void launch_conv_bwd(const ConvBwd &P, int W, bool vec, cudaStream_t st) {
         constexpr int WW = decltype(w)::value, th = 32 * kConvBwdWarps;
         if (vec)
             conv_launch(conv_bwd_kernel<T, ST, DT, GT, WW, true>, P, grid, th,
-                        kConvBwdWarps * (Stream<T, true>::BYTES + Stream<DT, true>::BYTES), st);
+                        kConvBwdWarps * (Stream<T, true>::WARP_BYTES + Stream<DT, true>::WARP_BYTES), st);
         else
             conv_launch(conv_bwd_kernel<T, ST, DT, GT, WW, false>, P, grid, th,
-                        kConvBwdWarps * (Stream<T, false>::BYTES + Stream<DT, false>::BYTES), st);
+                        kConvBwdWarps * (Stream<T, false>::WARP_BYTES + Stream<DT, false>::WARP_BYTES), st);
     });
 }
 

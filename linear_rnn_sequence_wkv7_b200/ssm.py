@@ -150,6 +150,13 @@ def _tokens(t, shape, dtype, dev, name, inner=1):
     return (t.data_ptr(), *st[:-inner])
 
 
+def _like(x, dtype):
+    """An uninitialised tensor of x's shape on its device."""
+    if dtype is x.dtype and x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, dtype=dtype, device=x.device)
+
+
 def _rows(t: torch.Tensor, name: str):
     """(rows, stride between rows) of a [..., D] tensor whose rows are evenly spaced."""
     D = t.shape[-1]
@@ -267,7 +274,7 @@ def rmsnorm_forward(x, weight, residual=None, *, eps=1e-6, out8=False, save8=Fal
             else:
                 yp, ysp = _act8_ptrs(y, shape, dev, "y")
         else:
-            y = torch.empty(shape, dtype=_out_dtype(y_dtype, x.dtype), device=dev) if y is None else y
+            y = _like(x, _out_dtype(y_dtype, x.dtype)) if y is None else y
             yc, yp, ysp = _code(y), _full(y, shape, y.dtype, dev, "y"), None
         if residual is not None and residual_out is None:
             residual_out = torch.empty_like(residual)
@@ -376,7 +383,7 @@ def conv_step(x, weight, bias, state, *, silu=True, y=None, y_dtype=None, stream
     xp, xb = _tokens(x, (B, D), x.dtype, dev, "x")
     with _on(x, stream):
         if y is None:
-            y = torch.empty((B, D), dtype=_out_dtype(y_dtype, x.dtype), device=dev)
+            y = _like(x, _out_dtype(y_dtype, x.dtype))
             yp = y.data_ptr()
         else:
             yp = _full(y, (B, D), y.dtype, dev, "y")
@@ -454,7 +461,7 @@ def _forward(u, delta, A, B, C, D, z, dt_bias, state0, softplus, lens, y, y_dtyp
     with _on(u, stream):
         Dn, N, G, args = _scan_args(u, delta, A, B, C, D, z, dt_bias)
         if y is None:
-            y = torch.empty((Bn, T, Dn), dtype=_out_dtype(y_dtype, u.dtype), device=dev)
+            y = _like(u, _out_dtype(y_dtype, u.dtype))
         if return_state and stateT is None:
             stateT = torch.empty((Bn, Dn, N), dtype=torch.float32, device=dev)
         if states is True:
@@ -504,7 +511,7 @@ def ssm_step(u, delta, A, B, C, state, D=None, z=None, dt_bias=None, *, softplus
     with _on(u, stream):
         Dn, N, G, args = _scan_args(u, delta, A, B, C, D, z, dt_bias)
         if y is None:
-            y = torch.empty((Bn, Dn), dtype=_out_dtype(y_dtype, u.dtype), device=dev)
+            y = _like(u, _out_dtype(y_dtype, u.dtype))
             yp = y.data_ptr()
         else:
             yp = _full(y, (Bn, Dn), y.dtype, dev, "y")

@@ -611,6 +611,37 @@ def test_captured_backward_replays(cuda_device):
             assert torch.equal(a, b)            # every sum in a fixed order
 
 
+def test_offsets_behind_two_to_the_31_elements(cuda_device):
+    """One sequence of 2^31 + elements: its last tokens are those of the same call on its last stretch."""
+    D = 2048
+    T = (1 << 31) // D + 4096
+    g = gen(51)
+    tail = 512
+    block = rand(g, tail, D, dtype=torch.bfloat16)
+    x = block.repeat(T // tail, 1)[None]
+    assert x.shape[1] == T and x.numel() > 1 << 31
+    last = x[:, -tail:]
+    w, cw, cb = rand(g, D), rand(g, D, 4, std=0.5), rand(g, D)
+    state = x[:, -tail - 3:-tail].contiguous()
+    assert torch.equal(ssm.conv_forward(x, cw, cb)[:, -tail:], ssm.conv_forward(last, cw, cb, state))
+    o, p = ssm.rmsnorm_forward(x, w, out8=True), ssm.rmsnorm_forward(last, w, out8=True)
+    assert torch.equal(ssm.act8_load(o.y)[:, -tail:], ssm.act8_load(p.y)) and torch.equal(o.rstd[:, -tail:], p.rstd)
+    del o
+    dx = ssm.conv_backward(x, cw, cb, x, grad_dtype=torch.bfloat16)[0]
+    assert torch.equal(dx[:, -tail:], ssm.conv_backward(last, cw, cb, last.contiguous(), state, grad_dtype=torch.bfloat16)[0])
+    del dx
+    # decays of e^-0.3 a token and more: a state forgets within 512 tokens
+    N = 4
+    A = -torch.exp(rand(g, D, N) * 0.1)
+    bc = rand(g, tail, 2 * N, dtype=torch.bfloat16).repeat(T // tail, 1)[None]
+    Bm, Cm = bc[..., :N].unflatten(-1, (1, N)), bc[..., N:].unflatten(-1, (1, N))
+    bias = torch.full((D,), 2.0, device="cuda")
+    y, h = ssm.ssm_forward(x, x, A, Bm, Cm, None, x, bias)
+    cut = lambda t: t[:, -2 * tail:]
+    y2, h2 = ssm.ssm_forward(cut(x), cut(x), A, cut(Bm), cut(Cm), None, cut(x), bias)
+    assert torch.equal(y[:, -tail:], y2[:, -tail:]) and torch.equal(h, h2)
+
+
 def test_empty_calls(cuda_device):
     v = scan_inputs(1, 2, 0, 16, 8, 1, "f32")
     y, h = ssm.ssm_forward(**v)

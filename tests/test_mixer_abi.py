@@ -27,6 +27,14 @@ def test_symbols(lib):
         assert hasattr(lib, name)
 
 
+def test_package_exports():
+    import linear_rnn_sequence_wkv7_b200 as pkg
+    for name in pkg._SSM_EXPORTS:
+        assert getattr(pkg, name) is getattr(ssm, name)
+    with pytest.raises(AttributeError):
+        pkg.no_such_operator
+
+
 def test_act8_refusals(lib):
     def save(rows=2, D=128, dt=BF16, x=P, ld=128, codes=P, scales=P):
         return lib.wkv7_act8_save(rows, D, dt, x, ld, codes, scales, None)
