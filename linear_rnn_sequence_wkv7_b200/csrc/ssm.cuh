@@ -162,7 +162,6 @@ template <int V> __device__ __forceinline__ void put_pairs(float2 *to, const flo
 // nor the loads of four channels in a row meet in a bank.
 template <int CC, int LN> struct Planes {
     static constexpr int PS = CC + 32 / LN, RS = LN * PS + (CC == 16 ? 16 : 0), FLOATS = kTile * RS;
-    static __device__ __forceinline__ void put(float *s, int k, int ch, int nl, float v) { s[k * RS + nl * PS + ch] = v; }
     template <int TC> static __device__ __forceinline__ void put(float *s, int k, int ch, int nl, const float (&v)[TC]) {
         storev<TC>(s + k * RS + nl * PS + ch, v);
     }
