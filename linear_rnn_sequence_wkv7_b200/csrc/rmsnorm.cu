@@ -134,7 +134,7 @@ template <typename F> __device__ __forceinline__ F block_add(F x, F *shared, int
 }
 
 // blocks of 128 a warp holds, and the threads of a row's block at most
-__host__ __device__ constexpr int norm_max_threads(int MB) { return MB == 1 ? 64 : MB == 2 ? 128 : MB == 4 ? 256 : 512; }
+__host__ __device__ constexpr int norm_max_threads(int MB) { return MB <= 2 ? 32 : 512; }
 // and the threads on an SM that the registers leave room for
 __host__ __device__ constexpr int norm_sm_threads(int MB) { return MB <= 2 ? 1024 : 512; }
 
@@ -490,8 +490,9 @@ rmsnorm_bwd_kernel(const NormBwd P) {
 }
 
 // A row's fixed work (the sum over warps, the root) costs a warp some 150
-// instructions, so a warp takes four blocks where the row has them.
-int norm_batch(int nblk) { return nblk <= 2 ? 1 : nblk <= 8 ? 2 : nblk <= 32 ? 4 : 8; }
+// instructions, so a warp takes four blocks where the row has them (32768 x 2048 to
+// 8 bits: 115 us, 175 at two; 16384 x 4096 122 us).
+int norm_batch(int nblk) { return nblk <= 2 ? nblk : nblk <= 64 ? 4 : 8; }
 
 int norm_threads(int nblk) { return 32 * ((nblk + norm_batch(nblk) - 1) / norm_batch(nblk)); }
 
@@ -513,11 +514,12 @@ wkv7_status norm_launch(K kernel, const P &p, long long grid, int threads, size_
 }
 // blocks of 128 a warp as a template argument; rows ahead where vector accesses
 // are allowed and an SM's shared memory holds them
-template <bool VEC, bool WIDE, typename F> wkv7_status by_batch(int nblk, int tensors, F &&f) {
+template <bool VEC, bool WIDE, int TENSORS, typename F> wkv7_status by_batch(int nblk, F &&f) {
     constexpr size_t kMost = 200 * 1024;
     auto ring = [&](auto mb) {
         if constexpr (VEC) {
-            if (ring_bytes<decltype(mb)::value, WIDE>(tensors, norm_threads(nblk)) <= kMost) return f(mb, std::true_type{});
+            if (ring_bytes<decltype(mb)::value, WIDE>(TENSORS, norm_threads(nblk)) <= kMost)
+                return f(mb, std::true_type{});
         }
         return f(mb, std::false_type{});
     };
@@ -526,7 +528,9 @@ template <bool VEC, bool WIDE, typename F> wkv7_status by_batch(int nblk, int te
         case 2: return ring(std::integral_constant<int, 2>{});
         case 4: return ring(std::integral_constant<int, 4>{});
     }
-    return f(std::integral_constant<int, 8>{}, std::false_type{});
+    // (the backward keeps dw in the shared memory that the rows would take)
+    if constexpr (TENSORS == 2) return ring(std::integral_constant<int, 8>{});
+    else return f(std::integral_constant<int, 8>{}, std::false_type{});
 }
 
 wkv7_status norm_dims(long long rows, int D) {
@@ -594,7 +598,7 @@ wkv7_status wkv7_rmsnorm_forward(long long rows, int D, wkv7_dtype x_dt, wkv7_dt
     const int nblk = blocks_of(D), threads = norm_threads(nblk);
     const bool narrow = x_dt == WKV7_BF16 && (!residual || r_dt == WKV7_BF16);
 #define WKV7_NORM(V, R)                                                                                     \
-    by_batch<V, R>(nblk, 2, [&](auto mb, auto ring) {                                                       \
+    by_batch<V, R, 2>(nblk, [&](auto mb, auto ring) {                                                       \
         constexpr int M = decltype(mb)::value;                                                              \
         constexpr bool G = decltype(ring)::value;                                                           \
         return norm_launch(rmsnorm_fwd_kernel<V, M, R, G>, P, grid, threads,                                \
@@ -639,7 +643,7 @@ wkv7_status wkv7_rmsnorm_backward(long long rows, int D, wkv7_dtype s_dt, wkv7_d
     const int nblk = blocks_of(D), threads = norm_threads(nblk);
     const bool narrow = s_dt != WKV7_F32 && dy_dt == WKV7_BF16 && (!dresidual || g_dt == WKV7_BF16);
 #define WKV7_NORM(V, R)                                                                                     \
-    by_batch<V, R>(nblk, 3, [&](auto mb, auto ring) {                                                       \
+    by_batch<V, R, 3>(nblk, [&](auto mb, auto ring) {                                                       \
         constexpr int M = decltype(mb)::value;                                                              \
         constexpr bool G = decltype(ring)::value;                                                           \
         return norm_launch(rmsnorm_bwd_kernel<V, M, R, G>, P, grid, threads,                                \
