@@ -16,8 +16,9 @@ inline int scan_pad(int N) { return N <= 8 ? 8 : N <= 16 ? 16 : N <= 32 ? 32 : 6
 __host__ __device__ constexpr int scan_channels(int NP) { return NP == 8 ? 32 : NP == 64 ? 8 : 16; }      // of a block
 __host__ __device__ constexpr int scan_threads(int NP, int TC) { return scan_channels(NP) * NP / (4 * TC); }
 
-// blocks of 2 scan_threads an SM that the registers must leave room for
-__host__ __device__ constexpr int scan_blocks(int NP, int TC) { return 20 * 16 / scan_threads(NP, TC); }
+// blocks of 2 scan_threads an SM that the registers must leave room for (the
+// summaries spill at 20 warps)
+__host__ __device__ constexpr int scan_blocks(int NP, int TC, bool y) { return (y ? 20 : 16) * 16 / scan_threads(NP, TC); }
 
 template <typename F> void by_pad(int NP, F &&f) {
     if (NP == 8) f(std::integral_constant<int, 8>{});

@@ -48,10 +48,9 @@ template <typename T, int NP, bool Y> struct ScanShared {
     float y[Y ? 2 : 1][Y ? Planes<CC, NP / 4>::FLOATS : 4];     // C . h, lane by lane
 };
 
-// V elements to shared memory: asynchronously, or through a register where they are two bytes
-template <int V, typename T> __device__ __forceinline__ void copy_in(T *to, const T *from) {
-    if constexpr (V * sizeof(T) >= 4) copy_async<V * (int)sizeof(T)>(to, from, true);
-    else *to = *from;
+template <typename T> __device__ __forceinline__ void put_raw(T *to, const Vec<T, 1> &v) {
+    if constexpr (sizeof(T) == 2) *reinterpret_cast<uint16_t *>(to) = (uint16_t)v.w[0];
+    else *reinterpret_cast<uint32_t *>(to) = v.w[0];
 }
 template <int V, typename T> __device__ __forceinline__ void shared_get(const T *p, float (&f)[V]) {
     Vec<T, V> v;
@@ -83,7 +82,7 @@ template <int THREADS> __device__ __forceinline__ int scan_flip() {
 }
 
 template <typename T, int NP, int TC, bool VEC, bool Y>
-__global__ void __launch_bounds__(2 * scan_threads(NP, TC), scan_blocks(NP, TC))
+__global__ void __launch_bounds__(2 * scan_threads(NP, TC), scan_blocks(NP, TC, Y))
 ssm_fwd_kernel(const ScanArgs P) {
     constexpr int CC = scan_channels(NP), LN = NP / 4, THREADS = scan_threads(NP, TC);     // of each kind
     constexpr int EPT = kTile * CC / THREADS, V = VEC ? (EPT < 4 ? EPT : 4) : 1, Q = EPT / V;   // a thread's share of a tile
@@ -144,26 +143,50 @@ ssm_fwd_kernel(const ScanArgs P) {
             if (j < nt) {
                 const int t = t0 + j * kTile, slot = j % kRing;
                 const bool full = t + kTile <= t1;      // uniform
+                if constexpr (V * sizeof(T) >= 4) {
 #pragma unroll
-                for (int q = 0; q < Q; ++q) {
-                    const int k = lt + q * QT;
-                    if (!full && t + k >= t1) continue;
-                    copy_in<V>(&s_in[slot][0][k][ch], pu + q * QT * P.u_ts);
-                    copy_in<V>(&s_in[slot][1][k][ch], pd + q * QT * P.d_ts);
-                    if (gate) copy_in<V>(&s_in[slot][NIN - 1][k][ch], pz + q * QT * P.z_ts);
+                    for (int q = 0; q < Q; ++q) {
+                        const int k = lt + q * QT;
+                        if (!full && t + k >= t1) continue;
+                        constexpr int BYTES = V * (int)sizeof(T);
+                        copy_async<BYTES>(&s_in[slot][0][k][ch], pu + q * QT * P.u_ts, true);
+                        copy_async<BYTES>(&s_in[slot][1][k][ch], pd + q * QT * P.d_ts, true);
+                        if (gate) copy_async<BYTES>(&s_in[slot][NIN - 1][k][ch], pz + q * QT * P.z_ts, true);
+                    }
+                } else {                                // too narrow for that: through registers, loads first
+                    static_assert(V == 1, "");
+                    Vec<T, 1> r[Q][3];
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        if (!full && t + lt + q * QT >= t1) continue;
+                        r[q][0].load(pu + q * QT * P.u_ts);
+                        r[q][1].load(pd + q * QT * P.d_ts);
+                        if (gate) r[q][2].load(pz + q * QT * P.z_ts);
+                    }
+#pragma unroll
+                    for (int q = 0; q < Q; ++q) {
+                        const int k = lt + q * QT;
+                        if (!full && t + k >= t1) continue;
+                        put_raw(&s_in[slot][0][k][ch], r[q][0]);
+                        put_raw(&s_in[slot][1][k][ch], r[q][1]);
+                        if (gate) put_raw(&s_in[slot][NIN - 1][k][ch], r[q][2]);
+                    }
                 }
+                Quad<T, false> v[VEC ? 1 : NB];
 #pragma unroll
                 for (int q = 0; q < NB; ++q) {
                     const int e = tid + q * THREADS, k = (e / (NP / 4)) % kTile, n = e % (NP / 4) * 4;
                     if (e >= (Y ? IB : IB / 2)) break;
                     const bool in = full || t + k < t1;
-                    T *to = &s_BC[slot][0][0][0] + 4 * e;
                     const T *from = (Y && e >= IB / 2 ? Cm + k * P.c_ts : Bm + k * P.b_ts) + n;
-                    if constexpr (VEC) copy_async<4 * (int)sizeof(T)>(to, from, in && n < P.N);
-                    else {
-                        Quad<T, false> v;
-                        v.load(from, in ? P.N - n : 0);
-                        v.put(to);
+                    if constexpr (VEC) copy_async<4 * (int)sizeof(T)>(&s_BC[slot][0][0][0] + 4 * e, from, in && n < P.N);
+                    else v[q].load(from, in ? P.N - n : 0);
+                }
+                if constexpr (!VEC) {
+#pragma unroll
+                    for (int q = 0; q < NB; ++q) {
+                        const int e = tid + q * THREADS;
+                        if (e < (Y ? IB : IB / 2)) v[q].put(&s_BC[slot][0][0][0] + 4 * e);
                     }
                 }
                 pu += kTile * P.u_ts, pd += kTile * P.d_ts, Bm += kTile * P.b_ts, Cm += kTile * P.c_ts;
