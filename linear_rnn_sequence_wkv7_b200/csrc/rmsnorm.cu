@@ -8,12 +8,11 @@
 // bf16 element).  A row is a block of warps; a warp owns blocks of 128 channels
 // (the 8-bit format's), MB of them held in registers between the sum and the
 // output, so the row is read once; the next two rows come through shared memory
-// meanwhile.  A row's fixed work (sum over the warps, root) is worth a third of
-// MB = 2's time, hence MB = 4 where the row has the blocks.
+// meanwhile.
 //
 // 32768 x 2048 bf16 with residual: 114 us to 8 bits (472 MB, 64% of the measured
-// copy rate; the exact sums and the sure codes cost 45 instructions an element,
-// and the schedulers issue 65% of cycles), 111 us to bf16 with the 8-bit copy of
+// copy rate; the exact sums and the sure codes cost 40 instructions an element,
+// and the schedulers issue 67% of cycles), 111 us to bf16 with the 8-bit copy of
 // the sum (606 MB, 84%), backward from the copy 89 us (473 MB, 82%).
 //
 // The 8-bit output rounds to 4 significant bits, and a value next to a border
