@@ -611,6 +611,117 @@ def test_captured_backward_replays(cuda_device):
             assert torch.equal(a, b)            # every sum in a fixed order
 
 
+def same(got, want):
+    for a, b in zip(got, want):
+        assert (a is None) == (b is None) and (a is None or torch.equal(a, b))
+
+
+def test_broadcast_and_shared_inputs(cuda_device):
+    """Inputs with stride 0, and one tensor as several inputs, equal the same call on copies: gradients are
+    those of each input by itself."""
+    B, T, D, N = 3, 37, 64, 16
+    v = scan_inputs(71, 1, T, D, N, 1, "bf16")
+    v["delta"] = v["delta"].contiguous()
+    per_token = ("u", "delta", "B", "C", "z")
+    wide = {k: t.expand(B, *t.shape[1:]) if k in per_token else t for k, t in v.items()}
+    wide["u"] = wide["u"][:, :1].expand(B, T, D)                # stride 0 over tokens too
+    wide["z"], wide["C"] = wide["delta"], wide["B"]
+    wide["state0"] = v["state0"].repeat(B, 1, 1)
+    flat = {k: t.clone(memory_format=torch.contiguous_format) for k, t in wide.items()}
+    same(ssm.ssm_forward(**wide), ssm.ssm_forward(**flat))
+    dy, dsT = rand(gen(72), B, T, D, dtype=torch.bfloat16), rand(gen(73), B, D, N)
+    same(ssm.ssm_backward(dy=dy, dstateT=dsT, **wide), ssm.ssm_backward(dy=dy, dstateT=dsT, **flat))
+    w, b = rand(gen(74), D, 4), rand(gen(75), D)
+    same(ssm.conv_forward(wide["u"], w, b, return_state=True), ssm.conv_forward(flat["u"], w, b, return_state=True))
+    same(ssm.conv_backward(wide["u"], w, b, dy), ssm.conv_backward(flat["u"], w, b, dy))
+
+
+@pytest.mark.parametrize("D", [256, 260, 131, 2048])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rmsnorm_slices_and_gradients_in_place(cuda_device, D, dtype):
+    """Rows cut out of wider ones, x as its own residual, dx over dresidual."""
+    g, dt = gen(76), DT[dtype]
+    x = rand(g, 5, 9, D + 16, dtype=dt)[..., 16:]
+    w, dy, dres = rand(g, D), rand(g, 5, 9, D, dtype=dt), rand(g, 5, 9, D, dtype=dt)
+    flat = x.contiguous()
+    a, b = ssm.rmsnorm_forward(x, w, save8=True), ssm.rmsnorm_forward(flat, w, save8=True)
+    same((a.y, a.rstd, *a.saved), (b.y, b.rstd, *b.saved))
+    twice, added = ssm.rmsnorm_forward(flat, w, flat), ssm.rmsnorm_forward(flat, w, flat.clone())
+    same((twice.y, twice.residual, twice.rstd), (added.y, added.residual, added.rstd))
+    want = ssm.rmsnorm_backward(dy, b.saved, b.rstd, w, dresidual=dres, grad_dtype=dt)
+    over = dres.clone()
+    got = ssm.rmsnorm_backward(dy, b.saved, b.rstd, w, dresidual=over, grad_dtype=dt, dx=over)
+    assert got[0] is over
+    same(got, want)
+
+
+def test_lengths_outside_the_batch_are_clamped(cuda_device):
+    B, T, D, N = 3, 700, 32, 16
+    v = scan_inputs(77, B, T, D, N, 1, "f32")
+    w = rand(gen(78), D, 4)
+    odd, plain = (torch.tensor(n, dtype=torch.int32, device="cuda") for n in ([-5, 2 ** 31 - 1, T + 1], [0, T, T]))
+    runs = []
+    for lens in (odd, plain):
+        y, c = torch.full((B, T, D), 3.0, device="cuda"), torch.full((B, T, D), 3.0, device="cuda")
+        st = ssm.conv_forward(v["u"], w, lens=lens, y=c, return_state=True)[1]
+        runs.append((y, ssm.ssm_forward(**v, lens=lens, y=y)[1], c, st))
+    same(*runs)
+    assert (runs[0][0][0] == 3.0).all() and (runs[0][2][0] == 3.0).all() and torch.equal(runs[0][1][0], v["state0"][0])
+
+
+def test_two_streams_at_once(cuda_device):
+    """The same operators on two streams at a time, each with its own inputs, give what they give alone."""
+    B, T, D, N = 2, 900, 128, 16
+    w, b, nw = rand(gen(79), D, 4), rand(gen(80), D), rand(gen(81), D)
+
+    def run(v, dy, stream=None):
+        u, kept = ssm.conv_forward(v["u"], w, b, save8=True, stream=stream)
+        y, _, states = ssm.ssm_forward_train(**dict(v, u=u), stream=stream)
+        g = ssm.ssm_backward(dy=dy, states=states, grad_dtype=torch.bfloat16, **dict(v, u=u), stream=stream)
+        c = ssm.conv_backward(kept, w, b, g.u, grad_dtype=torch.bfloat16, stream=stream)
+        n = ssm.rmsnorm_forward(y, nw, save8=True, stream=stream)
+        return (*g, *c, *ssm.rmsnorm_backward(dy, n.saved, n.rstd, nw, stream=stream))
+
+    sets = [(scan_inputs(82 + i, B, T, D, N, 1, "bf16"), rand(gen(90 + i), B, T, D, dtype=torch.bfloat16)) for i in range(2)]
+    alone = [run(*s) for s in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sets]
+    both = [[run(*s, stream=st) for s, st in zip(sets, streams)] for _ in range(3)]
+    torch.cuda.synchronize()
+    for pair in both:
+        for got, want in zip(pair, alone):
+            same(got, want)
+
+
+def test_captured_training_step_replays(cuda_device):
+    """Convolution and norm, forward to backward, from one graph that is replayed on other inputs."""
+    B, T, D = 2, 130, 256
+    g = gen(95)
+    w, b, nw = rand(g, D, 4), rand(g, D), rand(g, D)
+    first, second = (rand(g, 2, B, T, D, dtype=torch.bfloat16) for _ in range(2))
+    inputs = first.clone()
+
+    def run():
+        x, dy = inputs[0], inputs[1]
+        y, kept = ssm.conv_forward(x, w, b, save8=True)
+        n = ssm.rmsnorm_forward(y, nw, x, save8=True)
+        dx, dnw = ssm.rmsnorm_backward(dy, n.saved, n.rstd, nw, grad_dtype=torch.bfloat16)
+        return (n.y, dnw, *ssm.conv_backward(kept, w, b, dx, grad_dtype=torch.bfloat16))
+
+    want_first = run()
+    inputs.copy_(second)
+    want_second = run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for data, want in ((first, want_first), (second, want_second)):
+        inputs.copy_(data)
+        graph.replay()
+        torch.cuda.synchronize()
+        same(got, want)
+
+
 def test_offsets_behind_two_to_the_31_elements(cuda_device):
     """One sequence of 2^31 + elements: its last tokens are those of the same call on its last stretch."""
     D = 2048
