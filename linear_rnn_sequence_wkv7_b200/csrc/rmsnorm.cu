@@ -595,7 +595,7 @@ wkv7_status wkv7_rmsnorm_forward(long long rows, int D, wkv7_dtype x_dt, wkv7_dt
                      aligned_to(residual, 4 * dtype_size(r_dt)) && aligned_to(residual_out, 4 * dtype_size(r_dt)) &&
                      aligned_to(y, 4 * dtype_size(y_dt)) && aligned_to(weight, 16) && aligned_to(s_codes, 4);
     const int nblk = blocks_of(D), threads = norm_threads(nblk);
-    const bool narrow = x_dt == WKV7_BF16 && (!residual || r_dt == WKV7_BF16);
+    const bool narrow = x_dt == WKV7_BF16 && ((!residual && !residual_out) || r_dt == WKV7_BF16);
 #define WKV7_NORM(V, R)                                                                                     \
     by_batch<V, R, 2>(nblk, [&](auto mb, auto ring) {                                                       \
         constexpr int M = decltype(mb)::value;                                                              \
