@@ -503,10 +503,15 @@ long long norm_grid(long long rows, int D) {
     return rows < most ? rows : most;
 }
 
+// What a kernel's dynamic shared memory may be at most.  The leave for it is a property of
+// the kernel, not of the launch: it is this one number in every call, since a call
+// that set its own size would take it from a call of a wider row on another host thread.
+constexpr size_t kNormSmem = 200 * 1024;
+
 template <typename K, typename P>
 wkv7_status norm_launch(K kernel, const P &p, long long grid, int threads, size_t smem, cudaStream_t st) {
     if (smem > 40 * 1024 &&         // 48 KiB with the kernel's own arrays need no leave
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kNormSmem) != cudaSuccess)
         return WKV7_ERR_CUDA;
     kernel<<<(unsigned)grid, threads, smem, st>>>(p);
     return launch_status();
@@ -514,10 +519,9 @@ wkv7_status norm_launch(K kernel, const P &p, long long grid, int threads, size_
 // blocks of 128 a warp as a template argument; rows ahead where vector accesses
 // are allowed and an SM's shared memory holds them
 template <bool VEC, bool WIDE, int TENSORS, typename F> wkv7_status by_batch(int nblk, F &&f) {
-    constexpr size_t kMost = 200 * 1024;
     auto ring = [&](auto mb) {
         if constexpr (VEC) {
-            if (ring_bytes<decltype(mb)::value, WIDE>(TENSORS, norm_threads(nblk)) <= kMost)
+            if (ring_bytes<decltype(mb)::value, WIDE>(TENSORS, norm_threads(nblk)) <= kNormSmem)
                 return f(mb, std::true_type{});
         }
         return f(mb, std::false_type{});

@@ -1,5 +1,7 @@
 """Calls of the state-space mixer's operators at the edges of what their header
 allows, against the formulas in 64 bits (tests/_mixer.py)."""
+import threading
+
 import pytest
 import torch
 
@@ -28,3 +30,42 @@ def test_rmsnorm_keeps_the_sum_without_a_residual(cuda_device, D, dtype, kept):
     assert st == 0
     assert torch.equal(out, x.to(DT[kept]))
     assert torch.equal(y, ssm.rmsnorm_forward(x, w, eps=1e-6).y)
+
+
+def test_norms_of_two_widths_from_two_threads(cuda_device):
+    """Widths of one kernel that take different amounts of shared memory, launched by two host threads at once
+    through the C calls: none is refused."""
+    fwd = ssm.load_library().wkv7_rmsnorm_forward
+    bwd = ssm.load_library().wkv7_rmsnorm_backward
+    stream = torch.cuda.current_stream().cuda_stream
+    failed, go = [], threading.Barrier(2)
+
+    def calls(D):
+        x, w = rand(gen(D), 4, D, dtype=BF16), torch.ones(D, device="cuda")
+        y, r, dx, dw = torch.empty_like(x), torch.empty(4, device="cuda"), torch.empty_like(x), torch.empty(D, device="cuda")
+        ws = torch.empty(ssm.rmsnorm_backward_workspace_size(4, D), dtype=torch.uint8, device="cuda")
+        keep = (x, w, y, r, dx, dw, ws)
+        b = ssm.BF16
+        a = (4, D, b, b, b, x.data_ptr(), D, None, w.data_ptr(), 1e-6, None, y.data_ptr(), None, None, None, r.data_ptr(), stream)
+        g = (4, D, b, b, b, x.data_ptr(), None, r.data_ptr(), w.data_ptr(), x.data_ptr(), None, dx.data_ptr(), dw.data_ptr(),
+             ws.data_ptr(), ws.numel(), stream)
+        return keep, a, g
+
+    def work(a, g):
+        go.wait()
+        for _ in range(10000):
+            if fwd(*a) != 0:
+                failed.append("forward")
+            if bwd(*g) != 0:
+                failed.append("backward")
+
+    sets = [calls(D) for D in (8192, 4096)]
+    threads = [threading.Thread(target=work, args=s[1:]) for s in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, f"{len(failed)} calls refused"
+    for (x, w, y, *_), *_ in sets:
+        assert torch.equal(y, ssm.rmsnorm_forward(x, w).y)
