@@ -70,7 +70,10 @@ WKV7_API wkv7_status wkv7_act8_load(long long rows, int D, const void *codes, co
  *   x            : rows of x_dtype, x_ld elements apart
  *   residual     : [rows, D] of r_dtype, or NULL (s = x)
  *   weight       : [D] fp32
- *   eps          : >= 0
+ *   eps          : >= 0; the mean square is taken in fp64, so a row may be as large or
+ *                  small as its type allows.  A row with an infinity has rstd = 0, and
+ *                  one with mean(s^2) + eps = 0, or so small that rstd is above fp32's
+ *                  range, has rstd = inf; y follows from the formula
  *   residual_out : [rows, D] of r_dtype (s rounded), or NULL; may be residual
  *   y            : [rows, D] of y_dtype; WKV7_E4M3 writes 8-bit codes, with
  *                  y_scales [rows, ceil(D / 128)] (NULL otherwise)

@@ -132,6 +132,29 @@ template <typename F> __device__ __forceinline__ F block_add(F x, F *shared, int
     return t;
 }
 
+// unit / sqrt(x) in two floats, value and rest: the root in fp32 and one Newton step in fp64
+__device__ __forceinline__ float2 rsqrt2(double x, double unit) {
+    const double r = (double)rsqrtf((float)x), inv = fma(0.5 * r, fma(-x * r, r, 1.0), r) * unit;
+    const float hi = (float)inv;
+    return make_float2(hi, (float)(inv - (double)hi));
+}
+// A row whose squares left fp32's range (above 2^63, or below 2^-50 with an eps below that
+// too; mean is infinite, tiny or NaN then): 1 / sqrt(mean square) from `sum`, a thread's
+// squares of the row times far_unit.  Out of line: rare, and inline it took registers
+// from every row.
+__device__ __forceinline__ bool far_mean(double mean) {         // not in [2^-100, 2^126]
+    return __float_as_uint((float)mean) - 0x0d800000u > 0x7e800000u - 0x0d800000u;
+}
+__device__ __forceinline__ float far_unit(double mean) { return mean > 1.0 ? 0x1p-68f : 0x1p100f; }
+__device__ __noinline__ float2 far_row(double sum, double mean, double inv_D, double eps, double *shared) {
+    const double unit = far_unit(mean);
+    sum = block_add(sum, shared, threadIdx.x >> 5, blockDim.x >> 5);
+    mean = fma(sum, inv_D, eps * unit * unit);
+    if (mean == 0.0 || isinf(mean)) return make_float2(rsqrtf((float)mean), 0.f);
+    const float2 r = rsqrt2(mean, unit);
+    return make_float2(r.x, isinf(r.x) ? 0.f : r.y);
+}
+
 // blocks of 128 a warp holds, and the threads of a row's block at most
 __host__ __device__ constexpr int norm_max_threads(int MB) { return MB <= 2 ? 32 : 512; }
 // and the threads on an SM that the registers leave room for
@@ -282,10 +305,21 @@ rmsnorm_fwd_kernel(const NormFwd P) {
         // two buffers in turn: a warp that is a row ahead does not overwrite sums still being read
         sum = block_add(sum, shared[turn], warp, warps);
         turn ^= 1;
-        // 1 / sqrt in fp32, and one Newton step in fp64
-        const double mean = fma(sum, P.inv_D, P.eps), r0 = (double)rsqrtf((float)mean);
-        const double inv = isinf(r0) ? r0 : fma(0.5 * r0, fma(-mean * r0, r0, 1.0), r0);
-        const float ih = (float)inv, il = isinf(r0) ? 0.f : (float)(inv - (double)ih);
+        const double mean = fma(sum, P.inv_D, P.eps);
+        float2 inv;
+        if (!__any_sync(0xffffffffu, far_mean(mean))) {         // uniform in the block; the vote tells the compiler so
+            inv = rsqrt2(mean, 1.0);
+        } else {
+            const float unit = far_unit(mean);
+            double far = 0;
+#pragma unroll
+            for (int m = 0; m < MB; ++m)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) far += (double)(s[m][i] * unit) * (double)(s[m][i] * unit);
+            inv = far_row(far, mean, P.inv_D, P.eps, shared[turn]);
+            turn ^= 1;
+        }
+        const float ih = inv.x, il = inv.y;
         if (P.rstd && threadIdx.x == 0) P.rstd[row] = ih;
         if (!KEEP) {
 #pragma unroll
@@ -308,8 +342,8 @@ rmsnorm_fwd_kernel(const NormFwd P) {
             float v[4];
 #pragma unroll
             for (int i = 0; i < 4; i += 2) {        // off by 3 half steps at most
-                const float2 t = __fmul2_rn(make_float2(s[m][i], s[m][i + 1]), make_float2(w[m][i], w[m][i + 1]));
-                const float2 u = __fmul2_rn(t, make_float2(ih, ih));
+                const float2 t = __fmul2_rn(make_float2(s[m][i], s[m][i + 1]), make_float2(ih, ih));
+                const float2 u = __fmul2_rn(t, make_float2(w[m][i], w[m][i + 1]));
                 v[i] = u.x, v[i + 1] = u.y;
             }
             sure[m] = act8_encode_sure(v, q[m], scale[m]);
@@ -322,8 +356,8 @@ rmsnorm_fwd_kernel(const NormFwd P) {
                 float v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float p = s[m][i] * w[m][i], pl = fmaf(s[m][i], w[m][i], -p);
-                    const float t = p * ih, tl = fmaf(p, ih, -t) + fmaf(pl, ih, p * il);
+                    const float p = s[m][i] * ih, pl = fmaf(s[m][i], il, fmaf(s[m][i], ih, -p));
+                    const float t = p * w[m][i], tl = fmaf(pl, w[m][i], fmaf(p, w[m][i], -t));
                     const float top = t + tl;
                     v[i] = to_odd(top, tl - (top - t));
                 }

@@ -6,7 +6,9 @@ import pytest
 import torch
 
 from linear_rnn_sequence_wkv7_b200 import ssm
-from tests.test_gpu_mixer import DT, gen, rand
+from tests import _mixer as ref
+from tests._mixer import U32, check, f64
+from tests.test_gpu_mixer import DT, gen, norm_ref, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -69,3 +71,54 @@ def test_norms_of_two_widths_from_two_threads(cuda_device):
     assert not failed, f"{len(failed)} calls refused"
     for (x, w, y, *_), *_ in sets:
         assert torch.equal(y, ssm.rmsnorm_forward(x, w).y)
+
+
+@pytest.mark.parametrize("D", [128, 131, 256, 640, 2048, 9000])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("residual", [True, False])
+def test_rmsnorm_rows_whose_squares_leave_fp32(cuda_device, D, dtype, residual):
+    """|s| from 1e-37 to 2e38 with eps = 0: the mean square is between 1e-75 and 1e76."""
+    size = torch.tensor([1.0, 1e25, 1e19, 4e37, 1e-19, 1e-25, 1e-37, 1e-30], dtype=torch.float64)
+    g = gen(D)
+    # a row's values span a factor of 4, so that the smallest are no subnormals
+    x = ((torch.rand(8, D, generator=g, dtype=torch.float64) + 0.5) * size[:, None]).to(DT[dtype]).cuda()
+    r = ((torch.rand(8, D, generator=g, dtype=torch.float64) + 0.5) * size[:, None]).to(DT[dtype]).cuda() if residual else None
+    w = rand(g, D)
+    s, rstd, y = norm_ref(f64(x), f64(r), f64(w), 0.0)
+    o = ssm.rmsnorm_forward(x, w, r, eps=0.0, save8=True)
+    # rstd as for ordinary rows, or half a step of a subnormal (2^-150) where the row's size is above 2^126
+    sub = 2.0 ** -150
+    check(o.rstd, rstd[:, 0], 4 * U32 * rstd[:, 0] + sub, "rstd")
+    check(o.y, y, (8 * U32 + sub / rstd) * y.abs(), "y")
+    assert torch.equal(f64(ssm.act8_load(o.saved, F32)), ref.act8(s)[0])
+    q = ssm.rmsnorm_forward(x, w, r, eps=0.0, out8=True).y
+    each = f64(q.scales).repeat_interleave(128, -1)[..., :D]
+    code = f64(ssm.act8_load(q, F32)) / each
+    a, b = (ref.e4m3_round(y * (1 + e) / each) for e in (-2.0 ** -22, 2.0 ** -22))
+    assert ((code == a) | (code == b)).all()
+    # the gradient from what was kept
+    dy = rand(g, 8, D, dtype=DT[dtype])
+    dx, dw = ssm.rmsnorm_backward(dy, o.saved, o.rstd, w)
+    rs, W, G = f64(o.rstd)[:, None], f64(w), f64(dy)
+    xh = f64(ssm.act8_load(o.saved, F32)) * rs
+    c, cM = (W * G * xh).mean(-1, keepdim=True), (W * G * xh).abs().mean(-1, keepdim=True)
+    check(dx, rs * (W * G - xh * c), 64 * U32 * rs * ((W * G).abs() + cM * xh.abs()), "dx")
+    check(dw, (G * xh).sum(0), 24 * U32 * (G * xh).abs().sum(0), "dw")
+
+
+@pytest.mark.parametrize("D", [128, 131, 640, 2048, 9000])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rmsnorm_row_with_an_infinity(cuda_device, D, dtype):
+    """1 / sqrt(inf) = 0: the finite elements give 0, the infinite one inf * 0 = NaN; NaN takes its whole row;
+    other rows are as they were."""
+    x, w = rand(gen(D), 4, D, dtype=DT[dtype]), torch.ones(D, device="cuda")
+    x[1, D // 3] = float("inf")
+    x[2, D // 2] = float("nan")
+    o = ssm.rmsnorm_forward(x, w, eps=1e-6)
+    q = ssm.act8_load(ssm.rmsnorm_forward(x, w, eps=1e-6, out8=True).y, F32)
+    assert o.rstd[1] == 0 and torch.isnan(o.rstd[2])
+    for y in (o.y, q):
+        assert torch.isnan(y[1, D // 3]) and int(torch.isnan(y[1]).sum()) == 1 and int((y[1] == 0).sum()) == D - 1
+        assert torch.isnan(y[2]).all()
+    plain = ssm.rmsnorm_forward(x[0::3].contiguous(), w, eps=1e-6)
+    assert torch.equal(o.y[0::3], plain.y) and torch.equal(o.rstd[0::3], plain.rstd)
