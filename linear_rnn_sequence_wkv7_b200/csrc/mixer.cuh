@@ -255,11 +255,13 @@ __device__ __forceinline__ void act8_encode_all(const float (&x)[K][4], uint32_t
 // The same where every value is known to within 2^-22 of itself only: false if a
 // code or the scale could depend on more, that is if the values a 2^-21 below and
 // above have other codes, amax is next to a power's border, or numbers are too
-// large or too small for the scale.  Uniform in the warp.
+// large or too small for the scale.  A block of zeros (among them the blocks that a
+// warp holds behind a row's end) or of NaN is sure: its codes are 0 or NaN.
+// Uniform in the warp.
 __device__ __forceinline__ bool act8_encode_sure(const float (&x)[4], uint32_t &codes, float &scale) {
     const uint32_t top = act8_top(x), e = act8_exponent(top);
     const float inv = __uint_as_float((254u - e) << 23);
-    const bool border = (top & 0x7fffffu) - 0x5ffff8u <= 16u || top > 0x7b000000u || top < 0x08000000u;
+    const bool border = (top & 0x7fffffu) - 0x5ffff8u <= 16u || top > 0x7b000000u || top - 1u < 0x08000000u - 1u;
     float lo[4], hi[4];
 #pragma unroll
     for (int i = 0; i < 4; i += 2) {

@@ -122,3 +122,17 @@ def test_rmsnorm_row_with_an_infinity(cuda_device, D, dtype):
         assert torch.isnan(y[2]).all()
     plain = ssm.rmsnorm_forward(x[0::3].contiguous(), w, eps=1e-6)
     assert torch.equal(o.y[0::3], plain.y) and torch.equal(o.rstd[0::3], plain.rstd)
+
+
+@pytest.mark.parametrize("D", [384, 640, 700])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rmsnorm_8_bit_blocks_of_zeros_and_nan(cuda_device, D, dtype):
+    """Blocks that are all zero or all NaN, by the weight, beside ordinary ones."""
+    x, w = rand(gen(D), 7, D, dtype=DT[dtype]), torch.ones(D, device="cuda")
+    w[:128], w[128:256] = 0.0, float("nan")
+    q = ssm.rmsnorm_forward(x, w, eps=1e-6, out8=True).y
+    v = ssm.act8_load(q, F32)
+    assert (v[:, :128] == 0).all() and torch.isnan(v[:, 128:256]).all()
+    assert (q.scales[:, :2] == 2.0 ** -117).all()
+    one = ssm.rmsnorm_forward(x, torch.ones(D, device="cuda"), eps=1e-6, out8=True).y
+    assert torch.equal(v[:, 256:], ssm.act8_load(one, F32)[:, 256:]) and torch.equal(q.scales[:, 2:], one.scales[:, 2:])
