@@ -113,7 +113,8 @@ __device__ __forceinline__ float rcp(float x) {
     return y;
 }
 // 1 / (1 + e^-x).  The exponent's rounding, |x| log2(e) 2^-24, is below a bf16
-// result's half step for every |x| < 88; PRECISE (fp32 results) uses expf.
+// result's half step for every |x| < 88; PRECISE (fp32 results; in the scan fp32
+// inputs as well) uses expf.
 template <bool PRECISE> __device__ __forceinline__ float sigmoid(float x) {
     return rcp(1.f + (PRECISE ? expf(-x) : ex2(-x * kLog2e)));
 }
@@ -126,8 +127,9 @@ template <bool PRECISE> __device__ __forceinline__ float2 sigmoid2(float2 x) {
 // log(1 + e^x) = max(x, 0) + log1p(e), e = e^-|x| in (0, 1]; log1p(e) / e by its
 // Chebyshev interpolant of degree 9 on [0, 1] (off by 6e-9 of the value, 1e-7
 // evaluated in fp32), which keeps small values exact where log(1 + e) would not.
-// Not PRECISE (bf16 inputs, which are off by 2^-9 themselves): e by one ex2, off
-// by |x| log2(e) 2^-24.  Two values at a time: one packed instruction a step.
+// Not PRECISE (bf16 inputs, which are off by 2^-9 themselves): e by one ex2, off by
+// |x| log2(e) 2^-24, no more than e moves by the rounding of x = delta + dt_bias to
+// fp32.  Two values at a time: one packed instruction a step.
 template <bool PRECISE> __device__ __forceinline__ float2 softplus2(float2 x) {
     float2 e;
     if constexpr (PRECISE) {

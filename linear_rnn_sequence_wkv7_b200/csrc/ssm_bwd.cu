@@ -57,7 +57,8 @@ struct BwdArgs {
 };
 
 // A segment's own adjoint (from zero behind it) and sum of dt
-template <typename T, int NP, bool VEC>
+// GATE: PRECISE of the gates and of the softplus's slope
+template <typename T, int NP, bool VEC, bool GATE>
 __global__ void __launch_bounds__(scan_threads(NP, 1))
 ssm_bwd_summary_kernel(const BwdArgs K) {
     const ScanArgs &P = K.f;
@@ -125,7 +126,7 @@ ssm_bwd_summary_kernel(const BwdArgs K) {
             if (P.softplus) softplus_all<PRECISE>(fd);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (z) fg[i] *= fz[i] * sigmoid<PRECISE>(fz[i]);
+                if (z) fg[i] *= fz[i] * sigmoid<GATE>(fz[i]);
                 fd[i] = in ? fd[i] : 0.f, fg[i] = in ? fg[i] : 0.f;
             }
             put_pairs<V>(&s_dd[k][lc - c0], fd, fg);
@@ -200,7 +201,7 @@ template <typename T, int NP> struct BwdShared {
     static constexpr int FLOATS = ACC + 2 * 4 * kBwdThreads;
 };
 
-template <typename T, int NP, bool VEC>
+template <typename T, int NP, bool VEC, bool GATE>
 __global__ void __launch_bounds__(kBwdThreads, 2)
 ssm_bwd_kernel(const BwdArgs K) {
     const ScanArgs &P = K.f;
@@ -292,7 +293,7 @@ ssm_bwd_kernel(const BwdArgs K) {
             if (P.softplus) softplus_all<PRECISE>(fd);
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                if (z) fg[i] *= fz[i] * sigmoid<PRECISE>(fz[i]);
+                if (z) fg[i] *= fz[i] * sigmoid<GATE>(fz[i]);
                 fd[i] = in ? fd[i] : 0.f, fu[i] = in ? fd[i] * fu[i] : 0.f, fg[i] = in ? fg[i] : 0.f;
             }
             put_pairs<V>(&s_dd[k][ch], fd, fu);
@@ -452,12 +453,12 @@ ssm_bwd_kernel(const BwdArgs K) {
                 const float ds = s_ds[k][ch + i], dt = s_dd[k][ch + i].x;
                 odu[i] = fmaf(dt, gb[i], skip[i] * ds);
                 float dd = fmaf(fu[i], gb[i], ap[i] * 0.6931471805599453f);     // a2 is in units of log 2
-                if (P.softplus) dd *= sigmoid<PRECISE>(fd[i] + bias[i]);
+                if (P.softplus) dd *= sigmoid<GATE>(fd[i] + bias[i]);
                 odd[i] = dd;
                 s_acc[i * THREADS + tid] += ds * fu[i];
                 s_acc[(V + i) * THREADS + tid] += dd;
                 if (z) {
-                    const float sg = sigmoid<PRECISE>(fz[i]);
+                    const float sg = sigmoid<GATE>(fz[i]);
                     odz[i] = fg[i] * fmaf(skip[i], fu[i], yc[i]) *
                              (sg * fmaf(fz[i], 1.f - sg, 1.f));
                 }
@@ -525,24 +526,24 @@ ssm_dbc_kernel(long long n, int tiles, const float *__restrict__ partial, GT *__
     else dC[i - n] = from_f32<GT>(s);
 }
 
-template <typename T, int NP, bool VEC>
+template <typename T, int NP, bool VEC, bool GATE>
 cudaError_t launch_bwd(const BwdArgs &K, const float *dstateT, cudaStream_t st) {
     const ScanArgs &P = K.f;
     BwdArgs M = K;
     M.exit = dstateT;
     if (P.nseg > 1) {
         const long long blocks = (long long)P.nseg * P.B * P.G * ((P.Dg + scan_channels(NP) - 1) / scan_channels(NP));
-        ssm_bwd_summary_kernel<T, NP, VEC><<<(unsigned)blocks, scan_threads(NP, 1), 0, st>>>(K);
+        ssm_bwd_summary_kernel<T, NP, VEC, GATE><<<(unsigned)blocks, scan_threads(NP, 1), 0, st>>>(K);
         const long long total = (long long)P.B * P.D * P.N;
         ssm_bwd_chain_kernel<<<(unsigned)((total + 255) / 256), 256, 0, st>>>(total, P.N, P.nseg, P.A, P.D, dstateT,
                                                                              K.seg_dt, K.seg_g);
         M.exit = K.seg_g;
     }
     constexpr size_t smem = BwdShared<T, NP>::FLOATS * sizeof(float);
-    const cudaError_t e =
-        cudaFuncSetAttribute(ssm_bwd_kernel<T, NP, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto kernel = ssm_bwd_kernel<T, NP, VEC, GATE>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    ssm_bwd_kernel<T, NP, VEC><<<(unsigned)((long long)P.nseg * P.B * P.G * P.tiles), kBwdThreads, smem, st>>>(M);
+    kernel<<<(unsigned)((long long)P.nseg * P.B * P.G * P.tiles), kBwdThreads, smem, st>>>(M);
     return cudaGetLastError();
 }
 
@@ -662,8 +663,15 @@ wkv7_status wkv7_ssm_backward(int B, int T, int D, int N, int G, wkv7_dtype in_d
     cudaError_t e = cudaSuccess;
     by_pad(scan_pad(N), [&](auto np) {
         constexpr int NP = decltype(np)::value;
-        if (in_dt == WKV7_F32) e = vec ? launch_bwd<float, NP, true>(K, dstateT, stream) : launch_bwd<float, NP, false>(K, dstateT, stream);
-        else e = vec ? launch_bwd<bf16, NP, true>(K, dstateT, stream) : launch_bwd<bf16, NP, false>(K, dstateT, stream);
+        auto launch = [&](auto t) {
+            using T = decltype(t);
+            by_precision<T>(K.g_f32, [&](auto gate) {
+                constexpr bool GATE = decltype(gate)::value;
+                e = vec ? launch_bwd<T, NP, true, GATE>(K, dstateT, stream) : launch_bwd<T, NP, false, GATE>(K, dstateT, stream);
+            });
+        };
+        if (in_dt == WKV7_F32) launch(float());
+        else launch(bf16());
     });
     if (e != cudaSuccess) return WKV7_ERR_CUDA;
     const long long n = (long long)B * T * G * N;

@@ -81,7 +81,8 @@ template <int THREADS> __device__ __forceinline__ int scan_flip() {
     return flip;
 }
 
-template <typename T, int NP, int TC, bool VEC, bool Y>
+// Y: outputs too, not a summary alone;  GATE: the gate's PRECISE
+template <typename T, int NP, int TC, bool VEC, bool Y, bool GATE>
 __global__ void __launch_bounds__(2 * scan_threads(NP, TC), scan_blocks(NP, TC, Y))
 ssm_fwd_kernel(const ScanArgs P) {
     constexpr int CC = scan_channels(NP), LN = NP / 4, THREADS = scan_threads(NP, TC);     // of each kind
@@ -229,7 +230,7 @@ ssm_fwd_kernel(const ScanArgs P) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) {
                         f[i] = fmaf(skip[i], fu[i], f[i]);
-                        if (gate) f[i] *= fz[i] * sigmoid<PRECISE>(fz[i]);
+                        if (gate) f[i] *= fz[i] * sigmoid<GATE>(fz[i]);
                     }
                     if (live && (full || t + k < t1)) {
                         if (P.y_f32) storev<V>(yf + (size_t)q * QT * P.D, f);
@@ -378,7 +379,7 @@ struct StepArgs {
 template <typename T, typename YT, int LN, int R, bool VEC>
 __global__ void __launch_bounds__(256, 4)
 ssm_step_kernel(const StepArgs P) {
-    constexpr bool PRECISE = sizeof(YT) == 4;
+    constexpr bool PRECISE = sizeof(T) == 4 || sizeof(YT) == 4;
     const long long unit = ((long long)blockIdx.x * 256 + threadIdx.x) / LN;
     const int nl = threadIdx.x % LN, ns = 4 * nl;
     if (unit >= P.total) return;                // LN lanes leave together
@@ -471,9 +472,14 @@ template <typename T, int NP, int TC, bool Y> void launch_fwd(const ScanArgs &P,
     const unsigned grid = (unsigned)((long long)P.nseg * P.B * P.G * P.tiles);
     constexpr int threads = 2 * scan_threads(NP, TC);
     constexpr size_t smem = sizeof(ScanShared<T, NP, Y>);
-    auto kernel = vec ? ssm_fwd_kernel<T, NP, TC, true, Y> : ssm_fwd_kernel<T, NP, TC, false, Y>;
-    if (smem > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    kernel<<<grid, threads, smem, st>>>(P);
+    auto launch = [&](auto gate) {
+        constexpr bool GATE = decltype(gate)::value;
+        auto kernel = vec ? ssm_fwd_kernel<T, NP, TC, true, Y, GATE> : ssm_fwd_kernel<T, NP, TC, false, Y, GATE>;
+        if (smem > 40 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        kernel<<<grid, threads, smem, st>>>(P);
+    };
+    if constexpr (Y) by_precision<T>(P.y_f32, launch);
+    else launch(std::false_type{});
 }
 // Two channels a thread halve the loads of B and C and the instructions around
 // them; one channel a thread makes twice the warps.  At N = 16 and 8 x 4096 tokens

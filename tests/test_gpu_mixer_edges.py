@@ -136,3 +136,43 @@ def test_rmsnorm_8_bit_blocks_of_zeros_and_nan(cuda_device, D, dtype):
     assert (q.scales[:, :2] == 2.0 ** -117).all()
     one = ssm.rmsnorm_forward(x, torch.ones(D, device="cuda"), eps=1e-6, out8=True).y
     assert torch.equal(v[:, 256:], ssm.act8_load(one, F32)[:, 256:]) and torch.equal(q.scales[:, 2:], one.scales[:, 2:])
+
+
+# ---- scan ----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [64, 67])
+@pytest.mark.parametrize("N", [4, 16, 40])
+def test_fp32_results_of_bf16_inputs(cuda_device, D, N):
+    """The gate and its gradients in fp32's precision for every z: with B = C = 0 and u = D = dy = 1 they are
+    all that is left; prompt and step alike."""
+    T = 3
+    z = torch.linspace(-60, 60, T * D).view(1, T, D).to(BF16).cuda()
+    one = torch.ones(1, T, D, dtype=BF16, device="cuda")
+    none = torch.zeros(1, T, 1, N, dtype=BF16, device="cuda")
+    A, skip = torch.full((D, N), -1.0, device="cuda"), torch.ones(D, device="cuda")
+    Z = f64(z)
+    sg = torch.sigmoid(Z)
+    # exp (2 steps, 4 roundings), sum, reciprocal (1 step), products: below 12 roundings, as conv_bound counts
+    gate, e = Z * sg, 12 * U32 * (Z * sg).abs()
+    y, _ = ssm.ssm_forward(one, one, A, none, none, skip, z, y_dtype=F32)
+    check(y, gate, e, "y")
+    for t in range(T):
+        st = torch.zeros(1, D, N, device="cuda")
+        yt = ssm.ssm_step(one[:, t], one[:, t], A, none[:, t], none[:, t], st, skip, z[:, t], y_dtype=F32)
+        check(yt, gate[:, t], e[:, t], "step")
+    g = ssm.ssm_backward(one, one, A, none, none, one, skip, z)
+    check(g.u, gate, e, "du")
+    check(g.z, sg * (1 + Z * (1 - sg)), 16 * U32 * sg * (1 + Z.abs() * (1 - sg)), "dz")
+    check(g.D, gate.sum((0, 1)), (e + T * U32 * gate.abs()).sum((0, 1)), "dD")
+
+
+@pytest.mark.parametrize("D", [64, 67])
+def test_fp32_step_size_gradients_of_bf16_inputs(cuda_device, D):
+    """One token, B = C = u = dy = 1 and no gate: ddelta is N sigmoid(delta)."""
+    N = 16
+    delta = torch.linspace(-60, 60, D).view(1, 1, D).to(BF16).cuda()
+    one = torch.ones(1, 1, D, dtype=BF16, device="cuda")
+    bc = torch.ones(1, 1, 1, N, dtype=BF16, device="cuda")
+    g = ssm.ssm_backward(one, delta, torch.full((D, N), -1.0, device="cuda"), bc, bc, one)
+    want = N * torch.sigmoid(f64(delta))
+    check(g.delta, want, 12 * U32 * want, "ddelta")
