@@ -19,6 +19,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // ---- V consecutive elements ---------------------------------------------------
 
+template <bool CONST, typename W> __device__ __forceinline__ W word(const W *p) {
+    if constexpr (CONST) return __ldg(p);
+    else return *p;
+}
 // Raw words first, values later: a batch of loads is issued before the first
 // conversion waits for one.
 template <typename T, int V> struct Vec {
@@ -28,17 +32,18 @@ template <typename T, int V> struct Vec {
 #pragma unroll
         for (int i = 0; i < (BYTES + 3) / 4; ++i) w[i] = 0;
     }
-    __device__ __forceinline__ void load(const T *p) {
-        if constexpr (BYTES == 1) w[0] = __ldg(reinterpret_cast<const uint8_t *>(p));
-        else if constexpr (BYTES == 2) w[0] = __ldg(reinterpret_cast<const uint16_t *>(p));
-        else if constexpr (BYTES == 4) w[0] = __ldg(reinterpret_cast<const uint32_t *>(p));
+    // CONST: nothing writes this memory during the kernel (a tensor that is updated in place is no such memory)
+    template <bool CONST = true> __device__ __forceinline__ void load(const T *p) {
+        if constexpr (BYTES == 1) w[0] = word<CONST>(reinterpret_cast<const uint8_t *>(p));
+        else if constexpr (BYTES == 2) w[0] = word<CONST>(reinterpret_cast<const uint16_t *>(p));
+        else if constexpr (BYTES == 4) w[0] = word<CONST>(reinterpret_cast<const uint32_t *>(p));
         else if constexpr (BYTES == 8) {
-            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(p));
+            const uint2 u = word<CONST>(reinterpret_cast<const uint2 *>(p));
             w[0] = u.x, w[1] = u.y;
         } else {
 #pragma unroll
             for (int i = 0; i < BYTES / 16; ++i) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+                const uint4 u = word<CONST>(reinterpret_cast<const uint4 *>(p) + i);
                 w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
             }
         }
@@ -291,12 +296,12 @@ template <typename T, bool VEC> struct Row4 {
 #pragma unroll
         for (auto &e : v) e.zero();
     }
-    __device__ __forceinline__ void load(const T *row, int blk, int lane, int D) {
+    template <bool CONST = true> __device__ __forceinline__ void load(const T *row, int blk, int lane, int D) {
 #pragma unroll
         for (int i = 0; i < (VEC ? 1 : 4); ++i) {
             v[i].zero();
             const int c = lane_channel<VEC>(blk, lane, i);
-            if (c < D) v[i].load(row + c);
+            if (c < D) v[i].template load<CONST>(row + c);
         }
     }
     __device__ __forceinline__ void get(float (&f)[4]) const {
@@ -311,10 +316,10 @@ template <typename T, bool VEC> struct Row4 {
         }
     }
 };
-template <bool VEC, typename T>
+template <bool VEC, bool CONST = true, typename T>
 __device__ __forceinline__ void row_load(const T *row, int blk, int lane, int D, float (&f)[4]) {
     Row4<T, VEC> r;
-    r.load(row, blk, lane, D);
+    r.template load<CONST>(row, blk, lane, D);
     r.get(f);
 }
 template <bool VEC, typename T>

@@ -36,14 +36,15 @@ template <bool WIDE, bool E, typename F> __device__ __forceinline__ void by_dtyp
     else if (!WIDE || dt == WKV7_BF16) f(bf16());
     else if constexpr (WIDE) f(float());
 }
-// MB blocks of a row, one branch around the batch
-template <bool VEC, int MB, bool WIDE, bool E>
+// MB blocks of a row, one branch around the batch.  Not CONST: residual and dresidual, which
+// may be outputs as well.
+template <bool VEC, int MB, bool WIDE, bool E, bool CONST = true>
 __device__ __forceinline__ void batch_load(const void *p, wkv7_dtype dt, int blk0, int step, int lane, int D,
                                            float (&f)[MB][4]) {
     by_dtype<WIDE, E>(dt, [&](auto t) {
         const decltype(t) *row = static_cast<const decltype(t) *>(p);
 #pragma unroll
-        for (int m = 0; m < MB; ++m) row_load<VEC>(row, blk0 + m * step, lane, D, f[m]);
+        for (int m = 0; m < MB; ++m) row_load<VEC, CONST>(row, blk0 + m * step, lane, D, f[m]);
     });
 }
 
@@ -227,7 +228,7 @@ rmsnorm_fwd_kernel(const NormFwd P) {
         };
         auto get_res = [&](float (&f)[MB][4]) {
             if constexpr (RING) ring.template get<false>(now, 1, P.r_dt, f);
-            else batch_load<VEC, MB, WIDE, false>(res.p, P.r_dt, warp, warps, lane, D, f);
+            else batch_load<VEC, MB, WIDE, false, false>(res.p, P.r_dt, warp, warps, lane, D, f);
         };
         auto error = [&](const float (&a)[4], const float (&b)[4], const float (&t)[4], float (&e)[4]) {
 #pragma unroll
@@ -502,7 +503,7 @@ rmsnorm_bwd_kernel(const NormBwd P) {
         if (P.dres) {
             if constexpr (RING) ring.template get<false>(now, 2, P.g_dt, g);
             else {
-                batch_load<VEC, MB, WIDE, false>(dr.p, P.g_dt, warp, warps, lane, D, g);
+                batch_load<VEC, MB, WIDE, false, false>(dr.p, P.g_dt, warp, warps, lane, D, g);
                 dr.next();
             }
 #pragma unroll

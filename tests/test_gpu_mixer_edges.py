@@ -176,3 +176,25 @@ def test_fp32_step_size_gradients_of_bf16_inputs(cuda_device, D):
     g = ssm.ssm_backward(one, delta, torch.full((D, N), -1.0, device="cuda"), bc, bc, one)
     want = N * torch.sigmoid(f64(delta))
     check(g.delta, want, 12 * U32 * want, "ddelta")
+
+
+# ---- in place ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("D", [131, 2050, 9000, 9001])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_rmsnorm_in_place_without_rows_ahead(cuda_device, D, dtype):
+    """residual_out over residual and dx over dresidual where rows are read straight from memory: the same as
+    into other tensors, with several rows a block and neighbouring rows in one cache line."""
+    rows = 3 * 148 + 5 if D >= 9000 else 3 * 592 + 5
+    g, dt = gen(D), DT[dtype]
+    x, r, w = rand(g, rows, D, dtype=dt), rand(g, rows, D, dtype=dt, std=1e4), rand(g, D)
+    x[::7] *= 2.0 ** -20            # sums that are not exact in fp32
+    want = ssm.rmsnorm_forward(x, w, r, save8=True)
+    over = r.clone()
+    got = ssm.rmsnorm_forward(x, w, over, save8=True, residual_out=over)
+    assert got.residual is over and torch.equal(over, want.residual) and torch.equal(got.y, want.y)
+    assert torch.equal(got.saved.codes.view(torch.uint8), want.saved.codes.view(torch.uint8))
+    dy = rand(g, rows, D, dtype=dt)
+    a = ssm.rmsnorm_backward(dy, want.saved, want.rstd, w, dresidual=r, grad_dtype=dt)
+    b = ssm.rmsnorm_backward(dy, want.saved, want.rstd, w, dresidual=(over := r.clone()), grad_dtype=dt, dx=over)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
