@@ -100,6 +100,12 @@ def _out_dtype(dtype, default: torch.dtype) -> torch.dtype:
     return dtype
 
 
+def _y_dtype(y, y_dtype):
+    """A given y's dtype is the call's; y_dtype beside it has to agree."""
+    if y_dtype is not None and y.dtype != y_dtype:
+        raise ValueError("y and y_dtype differ")
+
+
 @contextlib.contextmanager
 def _entered(dev, stream):
     with torch.cuda.device(dev):
@@ -265,6 +271,8 @@ def rmsnorm_forward(x, weight, residual=None, *, eps=1e-6, out8=False, save8=Fal
     rc = xc if residual is None else _code(residual)
     if out8 and y_dtype is not None:
         raise ValueError("y_dtype: not with out8")
+    if y is not None and out8 != isinstance(y, Act8):
+        raise ValueError("y: an Act8 with out8, a tensor without")
     with _on(x, stream):
         if out8:
             yc = E4M3
@@ -274,7 +282,10 @@ def rmsnorm_forward(x, weight, residual=None, *, eps=1e-6, out8=False, save8=Fal
             else:
                 yp, ysp = _act8_ptrs(y, shape, dev, "y")
         else:
-            y = _like(x, _out_dtype(y_dtype, x.dtype)) if y is None else y
+            if y is None:
+                y = _like(x, _out_dtype(y_dtype, x.dtype))
+            else:
+                _y_dtype(y, y_dtype)
             yc, yp, ysp = _code(y), _full(y, shape, y.dtype, dev, "y"), None
         if residual is not None and residual_out is None:
             residual_out = torch.empty_like(residual)
@@ -354,8 +365,8 @@ def conv_forward(x: Union[torch.Tensor, Act8], weight, bias=None, state=None, *,
         if y is None:
             y = torch.empty(shape, dtype=_out_dtype(y_dtype, torch.bfloat16 if isinstance(x, Act8) else x.dtype),
                             device=dev)
-        elif y_dtype is not None and y.dtype != y_dtype:
-            raise ValueError("y and y_dtype differ")
+        else:
+            _y_dtype(y, y_dtype)
         xc, (xp, xb, xt), xs, sdt = _conv_x(x, dev, y.dtype, shape)
         if return_state and state_out is None:
             state_out = torch.empty((B, W - 1, D), dtype=sdt, device=dev)
@@ -386,6 +397,7 @@ def conv_step(x, weight, bias, state, *, silu=True, y=None, y_dtype=None, stream
             y = _like(x, _out_dtype(y_dtype, x.dtype))
             yp = y.data_ptr()
         else:
+            _y_dtype(y, y_dtype)
             yp = _full(y, (B, D), y.dtype, dev, "y")
         st = lib.wkv7_conv_step(B, D, W, _code(x), _code(y), xp, xb, _full(weight, (D, W), torch.float32, dev, "weight"),
                                 _full(bias, (D,), torch.float32, dev, "bias"),
@@ -462,6 +474,8 @@ def _forward(u, delta, A, B, C, D, z, dt_bias, state0, softplus, lens, y, y_dtyp
         Dn, N, G, args = _scan_args(u, delta, A, B, C, D, z, dt_bias)
         if y is None:
             y = _like(u, _out_dtype(y_dtype, u.dtype))
+        else:
+            _y_dtype(y, y_dtype)
         if return_state and stateT is None:
             stateT = torch.empty((Bn, Dn, N), dtype=torch.float32, device=dev)
         if states is True:
@@ -514,6 +528,7 @@ def ssm_step(u, delta, A, B, C, state, D=None, z=None, dt_bias=None, *, softplus
             y = _like(u, _out_dtype(y_dtype, u.dtype))
             yp = y.data_ptr()
         else:
+            _y_dtype(y, y_dtype)
             yp = _full(y, (Bn, Dn), y.dtype, dev, "y")
         st = lib.wkv7_ssm_step(Bn, Dn, N, G, _code(u), _code(y), *args,
                                _full(state, (Bn, Dn, N), torch.float32, dev, "state"), softplus, yp, _raw(u))

@@ -198,3 +198,27 @@ def test_rmsnorm_in_place_without_rows_ahead(cuda_device, D, dtype):
     a = ssm.rmsnorm_backward(dy, want.saved, want.rstd, w, dresidual=r, grad_dtype=dt)
     b = ssm.rmsnorm_backward(dy, want.saved, want.rstd, w, dresidual=(over := r.clone()), grad_dtype=dt, dx=over)
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+# ---- refusals --------------------------------------------------------------------------
+
+def test_output_type_beside_an_output_has_to_agree(cuda_device):
+    """y decides its own type; a y_dtype that differs, or a y of the wrong form, is refused by every call."""
+    B, T, D, N = 2, 3, 16, 8
+    one = lambda *s, dt=BF16: torch.zeros(s, dtype=dt, device="cuda")
+    x, w, cw, A = one(B, T, D), one(D, dt=F32), one(D, 4, dt=F32), one(D, N, dt=F32)
+    bc, st, cs = one(B, T, 1, N), one(B, D, N, dt=F32), one(B, 3, D)
+    calls = [lambda **k: ssm.rmsnorm_forward(x, w, **k).y, lambda **k: ssm.conv_forward(x, cw, **k),
+             lambda **k: ssm.ssm_forward(x, x, A, bc, bc, **k)[0], lambda **k: ssm.ssm_forward_train(x, x, A, bc, bc, **k)[0]]
+    steps = [lambda **k: ssm.conv_step(x[:, 0], cw, None, cs, **k),
+             lambda **k: ssm.ssm_step(x[:, 0], x[:, 0], A, bc[:, 0], bc[:, 0], st, **k)]
+    for f, shape in [(f, (B, T, D)) for f in calls] + [(f, (B, D)) for f in steps]:
+        for dt in (F32, BF16):
+            y = one(*shape, dt=dt)
+            assert f(y=y) is y and f(y=y, y_dtype=dt) is y
+            with pytest.raises(ValueError):
+                f(y=y, y_dtype=F32 if dt is BF16 else BF16)
+    with pytest.raises(ValueError):
+        ssm.rmsnorm_forward(x, w, out8=True, y=one(B, T, D))
+    with pytest.raises(ValueError):
+        ssm.rmsnorm_forward(x, w, y=ssm.act8_save(x))
