@@ -41,6 +41,7 @@
 // gamma_t = prod_{m<=t} w_m times gamma_t; dw_m = sum_{t>=m} dL/dgamma_t
 // gamma_t / w_m.)
 #include "common.cuh"
+#include "status.cuh"
 
 namespace wkv7 {
 

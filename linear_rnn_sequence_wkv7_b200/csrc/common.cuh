@@ -18,14 +18,6 @@ constexpr int kN = 64;  // head size the kernels implement
 // then the lo image; counted in 16-byte words.
 constexpr int kMqChunkVec = 2 * 96 * kN * 2 / 16;
 
-// Sticky device-side status word (one per device): kernels that detect a
-// bounded wait running out or an out-of-domain chunk set it with atomicMax;
-// wkv7_get_device_status reads and clears it.  Defined here because the
-// library is compiled as a single translation unit (csrc/libwkv7.cu).
-__device__ int g_device_status = 0;
-
-__device__ __forceinline__ void raise_status(int code) { atomicMax(&g_device_status, code); }
-
 // Optional output epilogue of the time-mix block (Paper Review: RWKV-7
 // "Goose", section "The approach": the receptance reads the state, the block
 // also attends to the current token without storing it, and the output is

@@ -1,6 +1,7 @@
-// Single translation unit of libwkv7.so: the sticky device status word is one
-// __device__ variable shared by every kernel, so all kernels are compiled
-// together (no relocatable device code needed).
+// The WKV7 operators of libwkv7.so, one translation unit: the sticky device status
+// word (status.cuh) is one __device__ variable shared by their kernels, so they are
+// compiled together (no relocatable device code needed).  The state-space mixer's
+// files, which have no such word, are units of their own.
 #include "wkv7_api.cu"
 #include "fwd_seq.cu"
 #include "step.cu"

@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include "common.cuh"
+#include "status.cuh"
 
 namespace wkv7 {
 namespace umma {

@@ -8,6 +8,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "status.cuh"
 
 namespace wkv7 {
 
