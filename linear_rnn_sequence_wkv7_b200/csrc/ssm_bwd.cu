@@ -202,7 +202,7 @@ template <typename T, int NP> struct BwdShared {
 };
 
 template <typename T, int NP, bool VEC, bool GATE>
-__global__ void __launch_bounds__(kBwdThreads, 2)
+__global__ void __launch_bounds__(kBwdThreads, 2)         // 255 registers; N > 32: shared memory for one
 ssm_bwd_kernel(const BwdArgs K) {
     const ScanArgs &P = K.f;
     using S = BwdShared<T, NP>;
@@ -554,7 +554,9 @@ int bwd_tiles(int D, int N, int G) {
 // Segments of a backward: two blocks an SM, if that makes at least two segments
 // (whose summaries cost about a fifth of a pass), each of at least 64 tokens.
 // N = 16, segments against one piece: 4 x 4096 x 2048 1.21 / 1.52 ms, 1 x 4096 x
-// 2048 0.30 / 1.45 ms, 1 x 256 x 2048 78 / 112 us.
+// 2048 0.30 / 1.45 ms, 1 x 256 x 2048 78 / 112 us.  (Two blocks fit up to N = 32; above
+// that a block's shared memory, 120 KB and more, leaves room for one, and the
+// segments run in two waves.)
 int bwd_segments(int B, int T, int D, int N, int G, int sms) {
     const long long blocks = (long long)B * G * bwd_tiles(D, N, G);
     if (blocks <= 0 || sms <= 0) return 1;

@@ -554,7 +554,8 @@ wkv7_status ssm_dims(int B, int T, int D, int N, int G) {
     if (B < 0 || T < 0 || D < 0 || N <= 0 || G <= 0) return WKV7_ERR_INVALID_ARG;
     if (D % G != 0) return WKV7_ERR_INVALID_ARG;
     if (N > 64 || D > WKV7_SSM_MAX_D || T > kMaxTokens) return WKV7_ERR_UNSUPPORTED;
-    // a launch has at most 16 channels a block and 16 * 148 segments when that leaves SMs idle
+    // blocks of a launch: one for 8 channels (N > 32; 16 or more otherwise, 16 to 128 in the backward), rounded
+    // up in each group; segments multiply them only where they are a few an SM
     if ((double)B * (D + 16.0 * G) > (double)kMaxGrid) return WKV7_ERR_UNSUPPORTED;
     return WKV7_OK;
 }
