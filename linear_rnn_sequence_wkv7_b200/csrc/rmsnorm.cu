@@ -10,10 +10,11 @@
 // output, so the row is read once; the next two rows come through shared memory
 // meanwhile.
 //
-// 32768 x 2048 bf16 with residual: 114 us to 8 bits (472 MB, 64% of the measured
-// copy rate; the exact sums and the sure codes cost 40 instructions an element,
-// and the schedulers issue 67% of cycles), 111 us to bf16 with the 8-bit copy of
-// the sum (606 MB, 84%), backward from the copy 89 us (473 MB, 82%).
+// 32768 x 2048 bf16 with residual: 117 us to 8 bits (472 MB, 62% of the measured
+// copy rate; the exact sums and the sure codes cost 41 instructions an element,
+// and the schedulers issue 66% of cycles), 113 us to bf16 with the 8-bit copy of
+// the sum (606 MB, 83%), 94 us to bf16 alone (537 MB, 88%), backward from the copy
+// 89 us (473 MB, 82%).
 //
 // The 8-bit output rounds to 4 significant bits, and a value next to a border
 // between two codes would fall on either side by fp32's rounding; the row's sum
@@ -525,7 +526,7 @@ rmsnorm_bwd_kernel(const NormBwd P) {
 
 // A row's fixed work (the sum over warps, the root) costs a warp some 150
 // instructions, so a warp takes four blocks where the row has them (32768 x 2048 to
-// 8 bits: 115 us, 175 at two; 16384 x 4096 122 us).
+// 8 bits: 115 us, 175 at two, when this was chosen).
 int norm_batch(int nblk) { return nblk <= 2 ? nblk : nblk <= 64 ? 4 : 8; }
 
 int norm_threads(int nblk) { return 32 * ((nblk + norm_batch(nblk) - 1) / norm_batch(nblk)); }

@@ -350,7 +350,8 @@ def conv_forward(x: Union[torch.Tensor, Act8], weight, bias=None, state=None, *,
                  stream=None):
     """y [B, T, D] of the causal convolution of x with weight [D, W] (fp32, W = 2,
     3 or 4), bias [D] fp32, after ``state`` [B, W - 1, D] (the inputs before the
-    first token; None = zeros).  ``lens`` [B] int32 ends sequences early.
+    first token; None = zeros).  ``lens`` [B] int32 ends sequences early: rows of
+    y behind a sequence's end stay as they are (unset in a y that is allocated here).
 
     Returns y, or a tuple (y, state_out, saved) of what was asked for:
     ``return_state`` adds the last W - 1 inputs, ``save8`` x as an Act8.  With an
@@ -502,7 +503,8 @@ def ssm_forward(u, delta, A, B, C, D=None, z=None, dt_bias=None, state0=None, *,
     u, delta, z [B, T, D] and B, C [B, T, G, N] of one dtype; A [D, N], D and
     dt_bias [D], state0 [B, D, N] fp32 (None = zeros; z None = no gate); N <= 64.
     ``lens`` [B] int32 ends sequences early: rows of y behind a sequence's end
-    stay as they are, and stateT is the state at its end."""
+    stay as they are (unset in a y that is allocated here), and stateT is the state
+    at its end."""
     y, stateT, _ = _forward(u, delta, A, B, C, D, z, dt_bias, state0, softplus, lens, y, y_dtype, stateT, None, workspace,
                             return_state, stream)
     return (y, stateT) if return_state else y
