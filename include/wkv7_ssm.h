@@ -122,7 +122,7 @@ WKV7_API wkv7_status wkv7_rmsnorm_backward(long long rows, int D, wkv7_dtype s_d
  *               for zeros
  *   lens      : [B] tokens of each sequence (clamped to 0 .. T), or NULL for T.
  *               Rows of y behind a sequence's end stay as they are.
- *   y         : [B, T, D] of y_dtype
+ *   y         : [B, T, D] of y_dtype; not x itself
  *   state_out : [B, W - 1, D] of x_dtype, the last W - 1 inputs of each
  *               sequence, or NULL; not with codes, and not `state` itself
  *   codes, scales : the 8-bit activation of x, written in the same pass, or
@@ -150,9 +150,9 @@ WKV7_API size_t wkv7_conv_backward_workspace_size(int B, int T, int D, int W);
  *                grad_dtype when x is codes
  *   dy         : [B, T, D] of dy_dtype, contiguous
  *   dstate_out : [B, W - 1, D] fp32, or NULL for zeros
- *   dx         : [B, T, D] of grad_dtype
+ *   dx         : [B, T, D] of grad_dtype; not x or dy itself
  *   dweight    : [D, W] fp32;  dbias : [D] fp32, or NULL
- *   dstate     : [B, W - 1, D] fp32, or NULL
+ *   dstate     : [B, W - 1, D] fp32, or NULL; not dstate_out itself
  */
 WKV7_API wkv7_status wkv7_conv_backward(int B, int T, int D, int W, wkv7_dtype x_dtype, wkv7_dtype dy_dtype,
                                         wkv7_dtype grad_dtype, const void *x, long long x_bs, long long x_ts,

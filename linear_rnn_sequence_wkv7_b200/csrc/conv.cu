@@ -634,6 +634,7 @@ wkv7_status wkv7_conv_forward(int B, int T, int D, int W, wkv7_dtype x_dt, wkv7_
         !aligned_to(state, dtype_size(s_dt)) || !aligned_to(state_out, dtype_size(s_dt)))
         return WKV7_ERR_INVALID_ARG;
     if (T == 0 && !state_out) return WKV7_OK;
+    if (T > 0 && y == x) return WKV7_ERR_INVALID_ARG;       // a run reads W - 1 tokens of the run before
     if (q8) x_bs = (long long)T * D, x_ts = D;
     const int run = conv_run(B, T, D), runs = T > 0 ? (T + run - 1) / run : 1;      // T = 0: the state alone
     const ConvFwd P{B, T, D, x, x_bs, x_ts, x_scales, weight, bias, state, lens, silu, y, state_out,
@@ -728,6 +729,7 @@ wkv7_status wkv7_conv_backward(int B, int T, int D, int W, wkv7_dtype x_dt, wkv7
         q8 != (x_scales != nullptr) || !f32_opt(x_scales) || !aligned_to(state, dtype_size(s_dt)))
         return WKV7_ERR_INVALID_ARG;
     if (dstate && dstate == dstate_out) return WKV7_ERR_INVALID_ARG;
+    if (dx == dy || dx == x) return WKV7_ERR_INVALID_ARG;   // runs read W - 1 tokens of their neighbours
     if (workspace == nullptr || !aligned_to(workspace, 16) ||
         workspace_bytes < wkv7_conv_backward_workspace_size(B, T, D, W))
         return WKV7_ERR_INVALID_ARG;

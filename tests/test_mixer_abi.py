@@ -155,3 +155,21 @@ def test_binding_refuses_cpu_tensors_and_wrong_types():
         ssm.act8_save(x.half())
     with pytest.raises(TypeError):
         ssm.act8_load(ssm.Act8(x, x), torch.float16)
+
+
+def test_conv_refuses_its_input_as_output(lib):
+    """Runs read tokens of their neighbours: y = x, dx = dy and dx = x would be a race.  Other pointers differ, so
+    nothing else is refused, and no GPU is needed for the refusal."""
+    x, w, dy, dw, ws = (ctypes.c_void_p(4096 * k) for k in range(1, 6))
+
+    def fwd(y):
+        return lib.wkv7_conv_forward(1, 4, 8, 4, BF16, BF16, x, 32, 8, None, w, None, None, None, 1, y, None, None, None, None)
+
+    def bwd(dx):
+        return lib.wkv7_conv_backward(1, 4, 8, 4, BF16, BF16, BF16, x, 32, 8, None, w, None, None, dy, None, 1, dx, dw, None,
+                                      None, ws, 1 << 40, None)
+
+    assert fwd(x) == INVALID
+    assert bwd(dy) == INVALID and bwd(x) == INVALID
+    # a call on no token writes nothing
+    assert lib.wkv7_conv_forward(1, 0, 8, 4, BF16, BF16, x, 0, 8, None, w, None, None, None, 1, x, None, None, None, None) == OK
