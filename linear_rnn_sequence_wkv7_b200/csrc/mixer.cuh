@@ -119,7 +119,8 @@ __device__ __forceinline__ float rcp(float x) {
 }
 // 1 / (1 + e^-x).  The exponent's rounding, |x| log2(e) 2^-24, is below a bf16
 // result's half step for every |x| < 88; PRECISE (fp32 results; in the scan fp32
-// inputs as well) uses expf.
+// inputs as well) uses expf.  (The fp32 parameter gradients of a call with bf16
+// gradients carry it: |z| log2(e) 2^-24 of a term, less than their sums collect.)
 template <bool PRECISE> __device__ __forceinline__ float sigmoid(float x) {
     return rcp(1.f + (PRECISE ? expf(-x) : ex2(-x * kLog2e)));
 }
